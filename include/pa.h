@@ -14,6 +14,10 @@
  *                         lookup) and the shared-prefix-aware decode order
  *   pa_decode             single-query attention of every sequence over its
  *                         cached tokens, gathered through its block table
+ *   pa_decode_int4, pa_reshape_and_cache_int4   the same over 4-bit caches
+ *   pa_rope               rotary positions on queries and keys
+ *   pa_rope_and_cache     rotary positions and the cache write in one kernel
+ *   pa_gather_cache       cached rows of any cache back as 16-bit rows
  *
  * Sources: "vLLM PagedAttention 大模型推理架构深度实战" (ybb.press) section 2.2
  * (16-token blocks, per-sequence block table mapping logical to physical
@@ -35,12 +39,14 @@
  *   is enqueued on `stream` (a cudaStream_t passed as void*; NULL is the
  *   legacy default stream) and the call returns.
  * - Element type of q, out, key and value: 16-bit, fp16 or bf16
- *   (pa_dims.dtype); caches hold the same type or FP8 E4M3 codes
- *   (pa_dims.kv_dtype).  Arithmetic is fp32; outputs round to nearest-even.
+ *   (pa_dims.dtype); caches hold the same type, FP8 E4M3 codes or 4-bit
+ *   codes (pa_dims.kv_dtype).  Arithmetic is fp32; outputs round to nearest-even.
  * - Layouts (row-major, contiguous):
  *     q, out         [num_seqs, num_heads, head_dim] ([num_seqs, q_len,
  *                    num_heads, head_dim] for pa_decode_ext)
  *     k/v cache      [num_blocks, num_kv_heads, block_size, head_dim]
+ *                    (4-bit: bytes [num_blocks, num_kv_heads, 8 * head_dim +
+ *                    64], see PA_INT4)
  *     block_tables   int32 [num_seqs, max_blocks_per_seq]
  *     context_lens   int32 [num_seqs]
  *     key, value     [num_tokens, num_kv_heads, head_dim]
@@ -81,7 +87,11 @@ typedef enum pa_status {
 typedef enum pa_dtype {
     PA_F16 = 0,
     PA_BF16 = 1,
-    PA_FP8_E4M3 = 2 /* KV caches only: OCP FP8 E4M3 codes, one fp32 scale per tensor */
+    PA_FP8_E4M3 = 2, /* KV caches only: OCP FP8 E4M3 codes, one fp32 scale per tensor */
+    PA_INT4 = 3      /* KV caches only: 4-bit codes with a scale and a lowest value per (token, KV head):
+                        a (block, KV head) chunk is 16 rows of head_dim / 2 bytes (element 2 i in the low
+                        nibble of byte i), then for each row two bf16 numbers (scale, low); an element is
+                        code * scale + low */
 } pa_dtype;
 
 /* Bits of the device error word (pa_device_error). */
@@ -103,7 +113,8 @@ typedef struct pa_dims {
     int64_t num_blocks;         /* NB: physical blocks in each cache */
     int32_t dtype;              /* pa_dtype of q, out, key, value (PA_F16 / PA_BF16) */
     int32_t kv_dtype;           /* pa_dtype of the K / V caches; 0 (= PA_F16) or the value of
-                                   dtype means "same as dtype", PA_FP8_E4M3 an FP8 cache */
+                                   dtype means "same as dtype", PA_FP8_E4M3 an FP8 cache,
+                                   PA_INT4 a 4-bit one */
 } pa_dims;
 
 /*
@@ -243,8 +254,8 @@ size_t pa_decode_ext_workspace_size(const pa_dims *dims, const pa_decode_opts *o
                                     int32_t partition_tokens);
 
 /*
- * Multi-token / sliding-window decode over a 16-bit or FP8 E4M3 cache
- * (dims->kv_dtype).  q and out are [num_seqs, q_len, num_heads, head_dim] in
+ * Multi-token / sliding-window decode over a 16-bit, FP8 E4M3 or 4-bit
+ * cache (dims->kv_dtype).  q and out are [num_seqs, q_len, num_heads, head_dim] in
  * dims->dtype.  The q_len query tokens of sequence s are its last q_len
  * tokens, already written to the cache: query i sits at position
  * p = context_lens[s] - q_len + i and attends to positions j with
@@ -265,6 +276,134 @@ pa_status pa_decode_ext(void *out, const void *q, const void *k_cache, const voi
                         int32_t num_kv_heads, const pa_dims *dims, const pa_decode_opts *opts,
                         int32_t max_context_len, int32_t partition_tokens, void *workspace,
                         size_t workspace_bytes, void *stream);
+
+/*
+ * Decode attention over 4-bit caches (dims->kv_dtype == PA_INT4): pa_decode
+ * with K_s[j] = code * scale + low of the row (j, KV head), V_s[j] likewise;
+ * about a quarter of the bytes of a 16-bit cache.  Every group size and
+ * head_dim runs on one kernel that feeds the codes to the matrix units as
+ * exact integers: the query is rounded to 11 significant bits under a
+ * power-of-two factor per row (exact for any 16-bit q within 2^22 of the
+ * row's largest |q|) and the softmax weight times the V scale to fp16
+ * (|error| <= 2^-11 of the weight), logits, sums and the output in fp32.
+ * partition_tokens: 0 = automatic.  Workspace as from
+ * pa_decode_workspace_size with the same dims.
+ */
+pa_status pa_decode_int4(void *out, const void *q, const void *k_cache, const void *v_cache,
+                         const int32_t *block_tables, const int32_t *context_lens, float scale,
+                         int32_t num_kv_heads, const pa_dims *dims, int32_t max_context_len,
+                         int32_t partition_tokens, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Cache write into 4-bit caches: for every token t with slot >= 0 and KV head
+ * h, with x = key[t, h, :] widened to fp32 and every operation rounded to
+ * nearest-even,
+ *     low   = bf16(min x)
+ *     scale = bf16((max x - low) / 15)
+ *     code  = clamp(round_half_even((x - low) / scale), 0, 15)   (0 where scale == 0)
+ * and the same for value.  A row with a NaN or an infinity gets scale and low
+ * NaN (code 0): it reads back as NaN.  One kernel on `stream`.
+ */
+pa_status pa_reshape_and_cache_int4(const void *key, const void *value, void *k_cache, void *v_cache,
+                                    const int64_t *slot_mapping, int32_t num_tokens, const pa_dims *dims,
+                                    void *stream);
+
+/*
+ * The inverse of the cache writes: for every token t with slot_mapping[t] >=
+ * 0 and every KV head h, key[t, h, :] becomes the cached row of that slot in
+ * dims->dtype (value likewise): a copy of a 16-bit cache's row; code * k_scale
+ * of an FP8 cache's; (code * scale + low) * k_scale of a 4-bit cache's, each
+ * operation in fp32, rounded once to the 16-bit type.  Rows of negative slots
+ * are left as they were; slots past the pool are skipped and flagged
+ * (PA_DEVERR_SLOT).  Several tokens may name one slot.  Scales are finite and
+ * positive, 1 for a 16-bit cache.  One kernel on `stream`.
+ */
+pa_status pa_gather_cache(void *key, void *value, const void *k_cache, const void *v_cache,
+                          const int64_t *slot_mapping, int32_t num_tokens, const pa_dims *dims, float k_scale,
+                          float v_scale, void *stream);
+
+/*
+ * Rotary positions.  With R = rotary_dim, f_i = inv_freq[i] (radians per
+ * position, i < R / 2) and theta = position * f_i, the pair (a, b) = (x[i],
+ * x[i + R/2]) of a head, or (x[2i], x[2i + 1]) when interleaved, becomes
+ *     (m (a cos theta - b sin theta),  m (b cos theta + a sin theta))
+ * with m = magnitude; dims R and beyond stay as they are.  `inverse` turns by
+ * -theta: with the same m that is the transpose of the forward map, so it
+ * takes the gradient of a rotated row to the gradient of the row.  Angles and
+ * their sines are computed in fp64 (a position of 10^6 keeps them exact to
+ * fp32), m cos and m sin are rounded to fp32 and applied in fp32; results are
+ * rounded once.
+ */
+typedef struct pa_rope_opts {
+    const double *inv_freq; /* DEVICE, [rotary_dim / 2]; see pa_rope_frequencies */
+    int32_t rotary_dim;     /* even, 2 .. head_dim */
+    int32_t interleaved;    /* 0: pairs (i, i + R/2); 1: pairs (2i, 2i + 1) */
+    int32_t inverse;        /* 0 or 1 */
+    double magnitude;       /* finite; 1 unless the context is extended by PA_ROPE_YARN */
+} pa_rope_opts;
+
+typedef enum pa_rope_scaling {
+    PA_ROPE_PLAIN = 0,  /* f_i = base^(-2i / R) */
+    PA_ROPE_LINEAR = 1, /* positions divided by factor: f_i / factor */
+    PA_ROPE_NTK = 2,    /* base * factor^(R / (R - 2)): the slowest pair as with LINEAR, the fastest unchanged */
+    PA_ROPE_BANDS = 3,  /* per pair by its wavelength w = 2 pi / f_i against the trained context C: unchanged below
+                           C / high_freq_factor, divided by factor above C / low_freq_factor, linear in C / w between */
+    PA_ROPE_YARN = 4    /* per pair by its turns within C: unchanged above beta_fast, divided by factor below
+                           beta_slow, a linear ramp over the pair index between; magnitude 0.1 ln(factor) + 1 */
+} pa_rope_scaling;
+
+typedef struct pa_rope_config {
+    int32_t rotary_dim;       /* even, >= 2 */
+    int32_t scaling;          /* pa_rope_scaling */
+    double base;              /* > 1 */
+    double factor;            /* >= 1; not used by PLAIN */
+    double original_context;  /* C > 0: BANDS and YARN */
+    double low_freq_factor;   /* BANDS: 0 < low < high */
+    double high_freq_factor;
+    double beta_fast;         /* YARN: beta_fast > beta_slow > 0 */
+    double beta_slow;
+} pa_rope_config;
+
+/* Host: the rotary_dim / 2 frequencies of `config` (inv_freq, HOST array, to
+ * be copied to the device once) and the magnitude that goes with them.
+ * PA_ERR_NULL, or PA_ERR_SHAPE for a value outside the ranges above. */
+pa_status pa_rope_frequencies(const pa_rope_config *config, double *inv_freq, double *magnitude);
+
+/*
+ * q_out[t, h, :] = rotate(q[t, h, :], positions[t]) for num_heads query heads
+ * and k_out = rotate(k) for num_kv_heads key heads of num_tokens tokens.
+ * q or k may be NULL (with its output): only the other is rotated.  Inputs
+ * have q_stride / k_stride elements between tokens (a multiple of 8, at least
+ * heads * head_dim: views of a fused projection) and contiguous heads;
+ * outputs are contiguous.  An output may be its own contiguous input (in
+ * place); any other overlap of an output with an input or with the other
+ * output is refused (PA_ERR_SHAPE).  dims: num_heads, num_kv_heads, head_dim
+ * and dtype are used.  positions: DEVICE int64.  One kernel on `stream`.
+ */
+pa_status pa_rope(void *q_out, const void *q, void *k_out, const void *k, const int64_t *positions,
+                  int32_t num_tokens, const pa_dims *dims, const pa_rope_opts *rope, int64_t q_stride,
+                  int64_t k_stride, void *stream);
+
+/*
+ * One step's rotation and cache write in one kernel: for every token t with
+ * slot = slot_mapping[t] >= 0,
+ *     q_out[t, h, :] = rotate(q[t, h, :], positions[t])      for query heads
+ *     cache row of slot <- rotate(key[t, h, :], positions[t])  (K cache)
+ *     cache row of slot <- value[t, h, :]                       (V cache)
+ * into a 16-bit, FP8 (divided by k_scale / v_scale, as
+ * pa_reshape_and_cache_fp8) or 4-bit cache (as pa_reshape_and_cache_int4);
+ * the rotated key goes to the cache's type from fp32, without a rounding to
+ * 16 bits between.  Tokens with a negative slot are padding: nothing of them
+ * is written, their q_out rows included.  A slot past the pool is flagged
+ * (PA_DEVERR_SLOT), its key and value are skipped and its query is rotated.
+ * Slots must be distinct.  q may be NULL (with q_out).  Strides, in-place q
+ * and overlaps as in pa_rope (v_stride likewise); scales are finite and
+ * positive, 1 unless the cache is FP8.
+ */
+pa_status pa_rope_and_cache(void *q_out, const void *q, const void *key, const void *value, void *k_cache,
+                            void *v_cache, const int64_t *slot_mapping, const int64_t *positions,
+                            int32_t num_tokens, const pa_dims *dims, const pa_rope_opts *rope, int64_t q_stride,
+                            int64_t k_stride, int64_t v_stride, float k_scale, float v_scale, void *stream);
 
 /*
  * Prefix caching, host side ("vLLM PagedAttention 大模型推理架构深度实战"

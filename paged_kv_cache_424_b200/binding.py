@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(_HERE, "libpa.so")
 PA_OK = 0
 STATUS = {0: "PA_OK", -1: "PA_ERR_NULL", -2: "PA_ERR_DTYPE", -3: "PA_ERR_SHAPE", -4: "PA_ERR_UNSUPPORTED",
           -5: "PA_ERR_WORKSPACE", -6: "PA_ERR_CUDA", -7: "PA_ERR_ALIGN", -8: "PA_ERR_MEMORY"}
-PA_F16, PA_BF16, PA_FP8_E4M3 = 0, 1, 2
+PA_F16, PA_BF16, PA_FP8_E4M3, PA_INT4 = 0, 1, 2, 3
 DEVERR = {1: "BLOCK_ID", 2: "CONTEXT", 4: "SLOT", 8: "COPY_PAIR", 16: "TIMEOUT", 32: "LAYOUT"}
 # torch dtypes accepted for an FP8 E4M3 cache (the codes as bytes, or torch's own e4m3fn type)
 FP8_CACHE_DTYPES = (torch.uint8, torch.float8_e4m3fn)
@@ -29,6 +29,8 @@ FP8_CACHE_DTYPES = (torch.uint8, torch.float8_e4m3fn)
 # The C entry points declared in include/pa.h, in declaration order.
 EXPORTS = ["pa_decode_workspace_size", "pa_decode_num_partitions", "pa_decode", "pa_decode_noalloc",
            "pa_decode_fp8", "pa_reshape_and_cache_fp8", "pa_decode_ext_workspace_size", "pa_decode_ext",
+           "pa_decode_int4", "pa_reshape_and_cache_int4", "pa_gather_cache", "pa_rope_frequencies", "pa_rope",
+           "pa_rope_and_cache",
            "pa_prefix_cache_create", "pa_prefix_cache_destroy", "pa_prefix_cache_match", "pa_prefix_cache_insert",
            "pa_prefix_cache_release", "pa_prefix_cache_evict", "pa_prefix_cache_stats", "pa_prefix_order",
            "pa_reshape_and_cache", "pa_copy_blocks", "pa_swap_blocks", "pa_check_wait_timeout", "pa_last_error",
@@ -56,6 +58,21 @@ class pa_decode_opts(ctypes.Structure):
                 ("v_scale", ctypes.c_float), ("seq_order", ctypes.c_void_p)]
 
 
+class pa_rope_opts(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("inverse", ctypes.c_int32), ("magnitude", ctypes.c_double)]
+
+
+class pa_rope_config(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("scaling", ctypes.c_int32), ("base", ctypes.c_double),
+                ("factor", ctypes.c_double), ("original_context", ctypes.c_double),
+                ("low_freq_factor", ctypes.c_double), ("high_freq_factor", ctypes.c_double),
+                ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double)]
+
+
+ROPE_SCALING = {"plain": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
+
+
 def _load(path: str = LIB_PATH):
     if not os.path.exists(path):
         raise LibraryMissing(f"{path} is not built; run `python -m paged_kv_cache_424_b200.build`")
@@ -80,6 +97,20 @@ def _load(path: str = LIB_PATH):
     lib.pa_decode_ext_workspace_size.restype = u64
     lib.pa_decode_ext.argtypes = [vp, vp, vp, vp, vp, vp, f32, i32, dp, op, i32, i32, vp, u64, vp]
     lib.pa_decode_ext.restype = ctypes.c_int
+    rp = ctypes.POINTER(pa_rope_opts)
+    f64p = ctypes.POINTER(ctypes.c_double)
+    lib.pa_decode_int4.argtypes = [vp, vp, vp, vp, vp, vp, f32, i32, dp, i32, i32, vp, u64, vp]
+    lib.pa_decode_int4.restype = ctypes.c_int
+    lib.pa_reshape_and_cache_int4.argtypes = [vp, vp, vp, vp, vp, i32, dp, vp]
+    lib.pa_reshape_and_cache_int4.restype = ctypes.c_int
+    lib.pa_gather_cache.argtypes = [vp, vp, vp, vp, vp, i32, dp, f32, f32, vp]
+    lib.pa_gather_cache.restype = ctypes.c_int
+    lib.pa_rope_frequencies.argtypes = [ctypes.POINTER(pa_rope_config), f64p, f64p]
+    lib.pa_rope_frequencies.restype = ctypes.c_int
+    lib.pa_rope.argtypes = [vp, vp, vp, vp, vp, i32, dp, rp, i64, i64, vp]
+    lib.pa_rope.restype = ctypes.c_int
+    lib.pa_rope_and_cache.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, dp, rp, i64, i64, i64, f32, f32, vp]
+    lib.pa_rope_and_cache.restype = ctypes.c_int
     ip = ctypes.POINTER(ctypes.c_int32)
     lp = ctypes.POINTER(ctypes.c_int64)
     lib.pa_prefix_cache_create.argtypes = [i64]
@@ -152,7 +183,19 @@ def _need_cuda(*ts: Optional[torch.Tensor]) -> None:
             raise ValueError("tensors must be contiguous CUDA tensors")
 
 
+def int4_cache_shape(num_blocks: int, num_kv_heads: int, head_dim: int) -> tuple:
+    """Shape of a 4-bit K or V pool (a uint8 tensor): per (block, KV head) the
+    16 rows' codes and then their (scale, low) pairs."""
+    return (num_blocks, num_kv_heads, 8 * head_dim + 64)
+
+
+def _is_int4(cache: torch.Tensor) -> bool:
+    return cache.dim() == 3 and cache.dtype == torch.uint8
+
+
 def _kv_code(cache: torch.Tensor) -> int:
+    if _is_int4(cache):
+        return PA_INT4
     return PA_FP8_E4M3 if cache.dtype in FP8_CACHE_DTYPES else _dtype_code(cache)
 
 
@@ -162,9 +205,19 @@ def make_dims(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int, b
                    kv_dtype)
 
 
+def _pool_shape(cache: torch.Tensor) -> tuple:
+    """(blocks, KV heads, block size, head_dim) of a pool."""
+    if _is_int4(cache):
+        NB, Hk, nbytes = cache.shape
+        if nbytes < 72 or (nbytes - 64) % 8:
+            raise ValueError("a 4-bit pool is uint8 [num_blocks, num_kv_heads, 8 * head_dim + 64]")
+        return NB, Hk, 16, (nbytes - 64) // 8
+    return tuple(cache.shape)
+
+
 def dims_of(q: torch.Tensor, k_cache: torch.Tensor, block_tables: torch.Tensor) -> pa_dims:
     S, H, D = q.shape
-    NB, Hk, B, D2 = k_cache.shape
+    NB, Hk, B, D2 = _pool_shape(k_cache)
     if D2 != D:
         raise ValueError("q and k_cache disagree on head_dim")
     MB = block_tables.shape[1] if block_tables.dim() == 2 else 0
@@ -173,13 +226,13 @@ def dims_of(q: torch.Tensor, k_cache: torch.Tensor, block_tables: torch.Tensor) 
 
 def cache_dims(k_cache: torch.Tensor, dtype: Optional[torch.dtype] = None) -> pa_dims:
     """Block geometry of a cache; `dtype` is the 16-bit type of the tokens
-    written into it (taken from the cache itself unless it is FP8)."""
-    NB, Hk, B, D = k_cache.shape
+    written into it (taken from the cache itself unless it is FP8 or 4-bit)."""
+    NB, Hk, B, D = _pool_shape(k_cache)
     kv = _kv_code(k_cache)
     if dtype is not None:
         code = _dtype_code(torch.empty(0, dtype=dtype))
     else:
-        code = PA_F16 if kv == PA_FP8_E4M3 else kv
+        code = PA_F16 if kv in (PA_FP8_E4M3, PA_INT4) else kv
     return make_dims(0, Hk, Hk, D, B, 0, NB, code, kv)
 
 
@@ -262,6 +315,26 @@ def pa_decode_fp8(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_c
     return out
 
 
+def pa_decode_int4(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float, num_kv_heads: int,
+                   max_context_len: int, partition_tokens: int = 0, workspace: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """pa_decode over 4-bit caches (uint8 tensors of int4_cache_shape): an
+    element is code * scale + low of its row."""
+    _need_cuda(out, q, k_cache, v_cache, block_tables, context_lens, workspace)
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise TypeError("block_tables and context_lens must be int32")
+    if not _is_int4(k_cache) or not _is_int4(v_cache):
+        raise TypeError("4-bit caches must be uint8 tensors of int4_cache_shape")
+    dims = dims_of(q, k_cache, block_tables)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = LIB.pa_decode_int4(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens),
+                            float(scale), int(num_kv_heads), ctypes.byref(dims), int(max_context_len),
+                            int(partition_tokens), _ptr(workspace), ws_bytes, _stream(stream))
+    _check(st)
+    return out
+
+
 def pa_decode_ext_workspace_size(dims: pa_dims, opts: pa_decode_opts, max_context_len: int,
                                  partition_tokens: int = 0) -> int:
     n = LIB.pa_decode_ext_workspace_size(ctypes.byref(dims), ctypes.byref(opts), int(max_context_len),
@@ -285,7 +358,7 @@ def pa_decode_ext(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_c
     """Multi-token / sliding-window decode: q and out are [S, q_len, H, D];
     query i of sequence s sits at position context_lens[s] - q_len + i and
     attends to its `window` most recent positions (all when 0).  The caches
-    may be 16-bit or FP8 E4M3 (uint8 / float8_e4m3fn)."""
+    may be 16-bit, FP8 E4M3 (uint8 / float8_e4m3fn) or 4-bit."""
     _need_cuda(out, q, k_cache, v_cache, block_tables, context_lens, workspace)
     if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
         raise TypeError("block_tables and context_lens must be int32")
@@ -404,6 +477,150 @@ def pa_reshape_and_cache(key: torch.Tensor, value: torch.Tensor, k_cache: torch.
     st = LIB.pa_reshape_and_cache(_ptr(key), _ptr(value), _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping),
                                   int(slot_mapping.numel()), ctypes.byref(dims), _stream(stream))
     _check(st)
+
+
+def _check_rows(cache: torch.Tensor, slots: torch.Tensor, *rows: torch.Tensor) -> None:
+    """[tokens, KV heads, head_dim] rows that go with `slots` and a pool."""
+    _, Hk, _, D = _pool_shape(cache)
+    if slots.dtype != torch.int64:
+        raise TypeError("slot_mapping must be int64")
+    for t in rows:
+        if tuple(t.shape) != (slots.numel(), Hk, D):
+            raise ValueError(f"key and value must be [{slots.numel()}, {Hk}, {D}], got {tuple(t.shape)}")
+
+
+def _check_pools(k_cache: torch.Tensor, v_cache: torch.Tensor) -> None:
+    if k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+        raise ValueError("k_cache and v_cache must have one shape and dtype")
+
+
+def pa_reshape_and_cache_int4(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                              slot_mapping: torch.Tensor, stream=None) -> None:
+    """The 4-bit row of slot_mapping[t] = the codes, scale and low of key[t] (and value[t]) for slot >= 0."""
+    _need_cuda(key, value, k_cache, v_cache, slot_mapping)
+    if not _is_int4(k_cache):
+        raise TypeError("4-bit caches must be uint8 tensors of int4_cache_shape")
+    _check_pools(k_cache, v_cache)
+    _check_rows(k_cache, slot_mapping, key, value)
+    if value.dtype != key.dtype:
+        raise TypeError("key and value must have one dtype")
+    dims = cache_dims(k_cache, key.dtype)
+    _check(LIB.pa_reshape_and_cache_int4(_ptr(key), _ptr(value), _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping),
+                                         int(slot_mapping.numel()), ctypes.byref(dims), _stream(stream)))
+
+
+def pa_gather_cache(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    slot_mapping: torch.Tensor, k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> None:
+    """key[t] (and value[t]) = the cached row of slot_mapping[t] in key's 16-bit
+    dtype, for slot >= 0; other rows stay as they are."""
+    _need_cuda(key, value, k_cache, v_cache, slot_mapping)
+    _check_pools(k_cache, v_cache)
+    _check_rows(k_cache, slot_mapping, key, value)
+    if value.dtype != key.dtype or (_kv_code(k_cache) < PA_FP8_E4M3 and k_cache.dtype != key.dtype):
+        raise TypeError("key, value and a 16-bit cache must have one dtype")
+    dims = cache_dims(k_cache, key.dtype)
+    _check(LIB.pa_gather_cache(_ptr(key), _ptr(value), _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping),
+                               int(slot_mapping.numel()), ctypes.byref(dims), float(k_scale), float(v_scale),
+                               _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# rotary positions
+# ---------------------------------------------------------------------------
+def pa_rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
+                        original_context: float = 0.0, low_freq_factor: float = 1.0, high_freq_factor: float = 4.0,
+                        beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """(inv_freq, magnitude) of a rotation of the first `rotary_dim` dims: a
+    float64 CPU tensor [rotary_dim / 2] (copy it to the device once) and a
+    float, both for pa_rope and pa_rope_and_cache.  `scaling` is one of
+    ROPE_SCALING: "plain", "linear", "ntk", "bands" or "yarn"."""
+    if scaling not in ROPE_SCALING:
+        raise ValueError(f"scaling {scaling!r}: one of {sorted(ROPE_SCALING)}")
+    cfg = pa_rope_config(int(rotary_dim), ROPE_SCALING[scaling], float(base), float(factor), float(original_context),
+                         float(low_freq_factor), float(high_freq_factor), float(beta_fast), float(beta_slow))
+    inv_freq = torch.zeros(max(1, int(rotary_dim) // 2), dtype=torch.float64)
+    magnitude = ctypes.c_double(1.0)
+    _check(LIB.pa_rope_frequencies(ctypes.byref(cfg),
+                                   ctypes.cast(inv_freq.data_ptr(), ctypes.POINTER(ctypes.c_double)),
+                                   ctypes.byref(magnitude)))
+    return inv_freq, magnitude.value
+
+
+def _token_rows(t: Optional[torch.Tensor], what: str) -> int:
+    """Elements between the tokens of a [tokens, heads, head_dim] tensor whose
+    heads are contiguous (a view of a fused projection may have gaps between tokens)."""
+    if t is None:
+        return 0
+    if not t.is_cuda or t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{what} must be a CUDA tensor [tokens, heads, head_dim] with contiguous heads")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _rope_opts(inv_freq: torch.Tensor, positions: torch.Tensor, tokens: int, interleaved: bool, inverse: bool,
+               magnitude: float) -> pa_rope_opts:
+    _need_cuda(inv_freq, positions)
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
+        raise TypeError("inv_freq must be float64 [rotary_dim / 2] (pa_rope_frequencies)")
+    if positions.dtype != torch.int64 or positions.numel() != tokens:
+        raise TypeError("positions must be int64, one per token")
+    return pa_rope_opts(inv_freq.data_ptr(), 2 * inv_freq.numel(), int(bool(interleaved)), int(bool(inverse)),
+                        float(magnitude))
+
+
+def _same(a: Optional[torch.Tensor], b: Optional[torch.Tensor], what: str) -> None:
+    if (a is None) != (b is None):
+        raise ValueError(f"{what} and its output go together")
+    if a is not None and (a.shape != b.shape or a.dtype != b.dtype):
+        raise ValueError(f"{what} and its output must have one shape and dtype")
+
+
+def pa_rope(q_out: Optional[torch.Tensor], q: Optional[torch.Tensor], k_out: Optional[torch.Tensor],
+            k: Optional[torch.Tensor], positions: torch.Tensor, inv_freq: torch.Tensor, interleaved: bool = False,
+            magnitude: float = 1.0, inverse: bool = False, stream=None) -> None:
+    """q_out = rotate(q), k_out = rotate(k) for [tokens, heads, head_dim]
+    queries and keys (either pair may be None).  Inputs may be views with a
+    gap between tokens; outputs are contiguous, or the contiguous input
+    itself.  `inverse` turns back: the gradient of the rotation."""
+    _same(q, q_out, "q")
+    _same(k, k_out, "k")
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q or k is needed")
+    qs, ks = _token_rows(q, "q"), _token_rows(k, "k")
+    _need_cuda(q_out, k_out)
+    if q is not None and k is not None and (q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2] or
+                                            q.dtype != k.dtype):
+        raise ValueError("q and k must have the same tokens, head_dim and dtype")
+    opts = _rope_opts(inv_freq, positions, x.shape[0], interleaved, inverse, magnitude)
+    dims = make_dims(0, 0 if q is None else q.shape[1], 0 if k is None else k.shape[1], x.shape[2], 16, 0, 1,
+                     _dtype_code(x))
+    _check(LIB.pa_rope(_ptr(q_out), _ptr(q), _ptr(k_out), _ptr(k), _ptr(positions), int(x.shape[0]),
+                       ctypes.byref(dims), ctypes.byref(opts), qs, ks, _stream(stream)))
+
+
+def pa_rope_and_cache(q_out: Optional[torch.Tensor], q: Optional[torch.Tensor], key: torch.Tensor,
+                      value: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping: torch.Tensor,
+                      positions: torch.Tensor, inv_freq: torch.Tensor, interleaved: bool = False,
+                      magnitude: float = 1.0, k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> None:
+    """q_out = rotate(q); the cache rows of slot_mapping[t] = rotate(key[t])
+    and value[t] in the pools' type (16-bit, FP8 E4M3 or 4-bit).  Tokens with a
+    negative slot are left out entirely.  q, key and value may be views of a
+    fused projection; q may be None."""
+    _same(q, q_out, "q")
+    qs, ks, vs = _token_rows(q, "q"), _token_rows(key, "key"), _token_rows(value, "value")
+    _need_cuda(q_out, k_cache, v_cache, slot_mapping)
+    _check_pools(k_cache, v_cache)
+    _check_rows(k_cache, slot_mapping, key, value)
+    if value.dtype != key.dtype or (_kv_code(k_cache) < PA_FP8_E4M3 and k_cache.dtype != key.dtype):
+        raise TypeError("key, value and a 16-bit cache must have one dtype")
+    if q is not None and (q.shape[0] != key.shape[0] or q.shape[2] != key.shape[2] or q.dtype != key.dtype):
+        raise ValueError("q and key must have the same tokens, head_dim and dtype")
+    opts = _rope_opts(inv_freq, positions, key.shape[0], interleaved, False, magnitude)
+    dims = cache_dims(k_cache, key.dtype)
+    dims.num_heads = 0 if q is None else q.shape[1]
+    _check(LIB.pa_rope_and_cache(_ptr(q_out), _ptr(q), _ptr(key), _ptr(value), _ptr(k_cache), _ptr(v_cache),
+                                 _ptr(slot_mapping), _ptr(positions), int(slot_mapping.numel()), ctypes.byref(dims),
+                                 ctypes.byref(opts), qs, ks, vs, float(k_scale), float(v_scale), _stream(stream)))
 
 
 def pa_copy_blocks(k_caches: Sequence[torch.Tensor], v_caches: Sequence[torch.Tensor],

@@ -4,10 +4,12 @@
 #include <cstdint>
 #include <cmath>
 #include <cstdio>
+#include <initializer_list>
 
 #include "../../include/pa.h"
 #include "pa_common.cuh"
 #include "pa_decode.h"
+#include "pa_int4.cuh"
 
 namespace {
 
@@ -38,14 +40,22 @@ constexpr int kAutoPartitionTc = 1024;
 constexpr int kMaxPartitionTokens = 32768;
 
 bool kv_fp8(const pa_dims *d) { return d->kv_dtype == PA_FP8_E4M3; }
-int32_t kv_elem_bytes(const pa_dims *d) { return kv_fp8(d) ? 1 : 2; }
+bool kv_int4(const pa_dims *d) { return d->kv_dtype == PA_INT4; }
+
+// Bytes of one block of K (or V): num_kv_heads chunks of 16 tokens.
+int64_t kv_block_bytes(const pa_dims *d) {
+    const int64_t chunk = kv_int4(d) ? pa::int4_chunk_bytes(d->head_dim) : (int64_t)16 * d->head_dim * (kv_fp8(d) ? 1 : 2);
+    return chunk * d->num_kv_heads;
+}
+
+bool good_scale(float s) { return s > 0.f && isfinite(s); }
 
 // Checks of the fields every call uses.  `attention` adds the query-side ones.
 pa_status check_dims(const pa_dims *d, bool attention) {
     if (!d) return fail(PA_ERR_NULL, "dims is NULL");
     if (d->dtype != PA_F16 && d->dtype != PA_BF16) return fail(PA_ERR_DTYPE, "dtype %d is not PA_F16/PA_BF16", d->dtype);
-    if (d->kv_dtype != 0 && d->kv_dtype != d->dtype && d->kv_dtype != PA_FP8_E4M3)
-        return fail(PA_ERR_DTYPE, "kv_dtype %d: must be 0, dtype (%d) or PA_FP8_E4M3", d->kv_dtype, d->dtype);
+    if (d->kv_dtype != 0 && d->kv_dtype != d->dtype && d->kv_dtype != PA_FP8_E4M3 && d->kv_dtype != PA_INT4)
+        return fail(PA_ERR_DTYPE, "kv_dtype %d: must be 0, dtype (%d), PA_FP8_E4M3 or PA_INT4", d->kv_dtype, d->dtype);
     if (d->num_kv_heads <= 0 || d->head_dim <= 0 || d->block_size <= 0 || d->num_blocks <= 0)
         return fail(PA_ERR_SHAPE, "num_kv_heads, head_dim, block_size and num_blocks must be positive");
     if (d->block_size != 16) return fail(PA_ERR_UNSUPPORTED, "block_size %d: only 16 is built", d->block_size);
@@ -88,6 +98,7 @@ int row_capacity(int rows) {
 // (measured on B200: over an FP8 cache 122 us against 273 us for the 7B MHA
 // batch, whose rows would pad the MMA's 16 columns).
 int tc_rows(const pa_dims *d, int rows) {
+    if (kv_int4(d)) return 0;  // 4-bit caches have a kernel of their own
     return pa::decode_tc_supported(d->head_dim, rows, d->num_blocks, d->num_kv_heads) ? rows : 0;
 }
 
@@ -248,6 +259,11 @@ pa_status decode_impl(void *out, const void *q, const void *k_cache, const void 
     const int rows = row_capacity(g * q_len);
     const int tc = tc_rows(dims, rows);
     const bool fp8 = kv_fp8(dims);
+    if (kv_int4(dims)) {
+        p.parts_per_cta = p.heads_per_cta = 1;
+        const cudaError_t e = pa::launch_decode_int4(p, dims->dtype, dims->head_dim, rows, static_cast<cudaStream_t>(stream));
+        return e == cudaSuccess ? PA_OK : cuda_fail(e, "pa_decode_int4 launch");
+    }
     p.parts_per_cta = tc ? tc_parts_per_cta(pl, dims->num_seqs, dims->num_kv_heads, tc, fp8) : 1;
     // the plain tensor-core variant: one query token, no window, unscaled 16-bit V
     const bool plain = tc && !fp8 && q_len == 1 && window == 0 && v_scale == 1.f;
@@ -276,6 +292,74 @@ pa_status check_opts(const pa_dims *d, const pa_decode_opts *o) {
     const int64_t rows = (int64_t)(d->num_heads / d->num_kv_heads) * o->q_len;
     if (rows > 16) return fail(PA_ERR_UNSUPPORTED, "group * q_len = %lld: at most 16 query rows per KV head",
                                (long long)rows);
+    return PA_OK;
+}
+
+// The byte range [lo, hi) a call reads or writes through one pointer.
+struct Range {
+    uintptr_t lo = 0, hi = 0;
+};
+Range range_of(const void *p, int64_t tokens, int64_t stride, int64_t row) {
+    Range r;
+    if (!p || tokens <= 0 || row <= 0) return r;
+    r.lo = reinterpret_cast<uintptr_t>(p);
+    r.hi = r.lo + 2 * (size_t)((tokens - 1) * stride + row);
+    return r;
+}
+bool meet(const Range &a, const Range &b) { return a.lo < b.hi && b.lo < a.hi; }
+
+pa_status check_stride(const char *what, int64_t stride, int64_t row) {
+    if (stride < row || stride % 8 != 0 || stride > ((int64_t)1 << 40))
+        return fail(PA_ERR_SHAPE, "%s %lld: must be a multiple of 8 elements, at least %lld", what, (long long)stride,
+                    (long long)row);
+    return PA_OK;
+}
+
+// Options of the rotation for heads of d->head_dim elements.
+pa_status check_rope(const pa_dims *d, const pa_rope_opts *r) {
+    if (!r) return fail(PA_ERR_NULL, "rope is NULL");
+    if (r->rotary_dim < 2 || r->rotary_dim % 2 != 0 || r->rotary_dim > d->head_dim)
+        return fail(PA_ERR_SHAPE, "rotary_dim %d: must be even, 2 .. head_dim (%d)", r->rotary_dim, d->head_dim);
+    if ((r->interleaved & ~1) || (r->inverse & ~1)) return fail(PA_ERR_SHAPE, "interleaved and inverse must be 0 or 1");
+    if (!isfinite(r->magnitude)) return fail(PA_ERR_SHAPE, "magnitude must be finite");
+    return PA_OK;
+}
+
+// Shared body of pa_rope and pa_rope_and_cache after their own checks:
+// strides, alignment, overlaps, and the parameters of the kernel.
+pa_status fill_rope(pa::RopeParams *p, void *q_out, const void *q, void *k_out, const void *k, const void *v,
+                    const int64_t *positions, int32_t num_tokens, const pa_dims *d, const pa_rope_opts *r,
+                    int64_t q_stride, int64_t k_stride, int64_t v_stride) {
+    const int64_t qrow = (int64_t)d->num_heads * d->head_dim, krow = (int64_t)d->num_kv_heads * d->head_dim;
+    pa_status st;
+    if (q && (st = check_stride("q_stride", q_stride, qrow)) != PA_OK) return st;
+    if (k && (st = check_stride("k_stride", k_stride, krow)) != PA_OK) return st;
+    if (v && (st = check_stride("v_stride", v_stride, krow)) != PA_OK) return st;
+    for (const void *ptr : {(const void *)q_out, q, (const void *)k_out, k, v})
+        if (!aligned16(ptr)) return fail(PA_ERR_ALIGN, "q, k, v and outputs must be 16-byte aligned");
+    const Range rq = range_of(q, num_tokens, q_stride, qrow), rk = range_of(k, num_tokens, k_stride, krow);
+    const Range rv = range_of(v, num_tokens, v_stride, krow);
+    const Range oq = range_of(q_out, num_tokens, qrow, qrow), ok = range_of(k_out, num_tokens, krow, krow);
+    const bool q_own = q_out == q && q_stride == qrow, k_own = k_out == k && k_stride == krow;
+    if ((!q_own && meet(oq, rq)) || meet(oq, rk) || meet(oq, rv) || (!k_own && meet(ok, rk)) || meet(ok, rq) || meet(oq, ok))
+        return fail(PA_ERR_SHAPE, "an output overlaps an input (in place needs the same contiguous tensor) or the other output");
+    p->q_out = q_out;
+    p->q = q;
+    p->k_out = k_out;
+    p->k = k;
+    p->v = v;
+    p->positions = positions;
+    p->inv_freq = r->inv_freq;
+    p->q_stride = q_stride;
+    p->k_stride = k_stride;
+    p->v_stride = v_stride;
+    p->num_tokens = num_tokens;
+    p->num_heads = q ? d->num_heads : 0;
+    p->num_kv_heads = k ? d->num_kv_heads : 0;
+    p->half = r->rotary_dim / 2;
+    p->interleaved = r->interleaved;
+    p->inverse = r->inverse;
+    p->magnitude = r->magnitude;
     return PA_OK;
 }
 
@@ -315,6 +399,7 @@ pa_status pa_decode(void *out, const void *q, const void *k_cache, const void *v
     pa_status st = check_dims(dims, true);
     if (st != PA_OK) return st;
     if (kv_fp8(dims)) return fail(PA_ERR_DTYPE, "pa_decode: kv_dtype is PA_FP8_E4M3, call pa_decode_fp8");
+    if (kv_int4(dims)) return fail(PA_ERR_DTYPE, "pa_decode: kv_dtype is PA_INT4, call pa_decode_int4");
     return decode_impl(out, q, k_cache, v_cache, block_tables, context_lens, scale, 1.f, 1.f, num_kv_heads, dims,
                        max_context_len, partition_tokens, workspace, workspace_bytes, stream);
 }
@@ -330,6 +415,17 @@ pa_status pa_decode_fp8(void *out, const void *q, const void *k_cache, const voi
         return fail(PA_ERR_SHAPE, "k_scale and v_scale must be finite and positive");
     return decode_impl(out, q, k_cache, v_cache, block_tables, context_lens, scale, k_scale, v_scale, num_kv_heads,
                        dims, max_context_len, partition_tokens, workspace, workspace_bytes, stream);
+}
+
+pa_status pa_decode_int4(void *out, const void *q, const void *k_cache, const void *v_cache,
+                         const int32_t *block_tables, const int32_t *context_lens, float scale, int32_t num_kv_heads,
+                         const pa_dims *dims, int32_t max_context_len, int32_t partition_tokens, void *workspace,
+                         size_t workspace_bytes, void *stream) {
+    pa_status st = check_dims(dims, true);
+    if (st != PA_OK) return st;
+    if (!kv_int4(dims)) return fail(PA_ERR_DTYPE, "pa_decode_int4: dims->kv_dtype must be PA_INT4");
+    return decode_impl(out, q, k_cache, v_cache, block_tables, context_lens, scale, 1.f, 1.f, num_kv_heads, dims,
+                       max_context_len, partition_tokens, workspace, workspace_bytes, stream);
 }
 
 size_t pa_decode_ext_workspace_size(const pa_dims *dims, const pa_decode_opts *opts, int32_t max_context_len,
@@ -364,7 +460,8 @@ pa_status pa_reshape_and_cache(const void *key, const void *value, void *k_cache
     if (!aligned16(key) || !aligned16(value) || !aligned16(k_cache) || !aligned16(v_cache))
         return fail(PA_ERR_ALIGN, "key, value and caches must be 16-byte aligned");
     if (kv_fp8(dims)) return fail(PA_ERR_DTYPE, "pa_reshape_and_cache: kv_dtype is PA_FP8_E4M3, call pa_reshape_and_cache_fp8");
-    pa::CacheDims cd{dims->num_kv_heads, dims->head_dim, dims->num_blocks, 2};
+    if (kv_int4(dims)) return fail(PA_ERR_DTYPE, "pa_reshape_and_cache: kv_dtype is PA_INT4, call pa_reshape_and_cache_int4");
+    pa::CacheDims cd{dims->num_kv_heads, dims->head_dim, dims->num_blocks, kv_block_bytes(dims)};
     cudaError_t e = pa::launch_reshape_and_cache(key, value, k_cache, v_cache, slot_mapping, num_tokens, cd,
                                                  static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "pa_reshape_and_cache launch");
@@ -384,7 +481,7 @@ pa_status pa_reshape_and_cache_fp8(const void *key, const void *value, void *k_c
     if (!key || !value || !k_cache || !v_cache || !slot_mapping) return fail(PA_ERR_NULL, "a required pointer is NULL");
     if (!aligned16(key) || !aligned16(value) || !aligned16(k_cache) || !aligned16(v_cache))
         return fail(PA_ERR_ALIGN, "key, value and caches must be 16-byte aligned");
-    pa::CacheDims cd{dims->num_kv_heads, dims->head_dim, dims->num_blocks, 1};
+    pa::CacheDims cd{dims->num_kv_heads, dims->head_dim, dims->num_blocks, kv_block_bytes(dims)};
     cudaError_t e = pa::launch_reshape_and_cache_fp8(key, value, k_cache, v_cache, slot_mapping, num_tokens, cd,
                                                      dims->dtype, k_scale, v_scale, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "pa_reshape_and_cache_fp8 launch");
@@ -404,10 +501,168 @@ pa_status pa_copy_blocks(void *const *k_caches, void *const *v_caches, int32_t n
             return fail(PA_ERR_ALIGN, "cache pointers of layer %d must be 16-byte aligned", i);
     }
     if (num_pairs > 65535) return fail(PA_ERR_SHAPE, "num_pairs %d > 65535", num_pairs);
-    pa::CacheDims cd{dims->num_kv_heads, dims->head_dim, dims->num_blocks, kv_elem_bytes(dims)};
+    pa::CacheDims cd{dims->num_kv_heads, dims->head_dim, dims->num_blocks, kv_block_bytes(dims)};
     cudaError_t e = pa::launch_copy_blocks(k_caches, v_caches, num_layers, block_mapping, num_pairs, cd,
                                            static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "pa_copy_blocks launch");
+    return PA_OK;
+}
+
+pa_status pa_reshape_and_cache_int4(const void *key, const void *value, void *k_cache, void *v_cache,
+                                    const int64_t *slot_mapping, int32_t num_tokens, const pa_dims *dims,
+                                    void *stream) {
+    pa_status st = check_dims(dims, false);
+    if (st != PA_OK) return st;
+    if (!kv_int4(dims)) return fail(PA_ERR_DTYPE, "pa_reshape_and_cache_int4: dims->kv_dtype must be PA_INT4");
+    if (num_tokens < 0) return fail(PA_ERR_SHAPE, "num_tokens %d < 0", num_tokens);
+    if (num_tokens == 0) return PA_OK;
+    if (!key || !value || !k_cache || !v_cache || !slot_mapping) return fail(PA_ERR_NULL, "a required pointer is NULL");
+    if (!aligned16(key) || !aligned16(value) || !aligned16(k_cache) || !aligned16(v_cache))
+        return fail(PA_ERR_ALIGN, "key, value and caches must be 16-byte aligned");
+    pa::RopeParams p{};
+    p.k = key;
+    p.v = value;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.slots = slot_mapping;
+    p.k_stride = p.v_stride = (int64_t)dims->num_kv_heads * dims->head_dim;
+    p.num_slots = dims->num_blocks * 16;
+    p.num_tokens = num_tokens;
+    p.num_kv_heads = dims->num_kv_heads;
+    p.k_scale = p.v_scale = 1.f;
+    cudaError_t e = pa::launch_rope(p, dims->dtype, dims->head_dim, PA_INT4, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "pa_reshape_and_cache_int4 launch");
+    return PA_OK;
+}
+
+pa_status pa_gather_cache(void *key, void *value, const void *k_cache, const void *v_cache,
+                          const int64_t *slot_mapping, int32_t num_tokens, const pa_dims *dims, float k_scale,
+                          float v_scale, void *stream) {
+    pa_status st = check_dims(dims, false);
+    if (st != PA_OK) return st;
+    if (!good_scale(k_scale) || !good_scale(v_scale))
+        return fail(PA_ERR_SHAPE, "k_scale and v_scale must be finite and positive");
+    if (!kv_fp8(dims) && !kv_int4(dims) && (k_scale != 1.f || v_scale != 1.f))
+        return fail(PA_ERR_SHAPE, "k_scale and v_scale must be 1 for a 16-bit cache");
+    if (num_tokens < 0) return fail(PA_ERR_SHAPE, "num_tokens %d < 0", num_tokens);
+    if (num_tokens == 0) return PA_OK;
+    if (!key || !value || !k_cache || !v_cache || !slot_mapping) return fail(PA_ERR_NULL, "a required pointer is NULL");
+    if (!aligned16(key) || !aligned16(value) || !aligned16(k_cache) || !aligned16(v_cache))
+        return fail(PA_ERR_ALIGN, "key, value and caches must be 16-byte aligned");
+    pa::GatherParams p{};
+    p.key = key;
+    p.value = value;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.slots = slot_mapping;
+    p.num_slots = dims->num_blocks * 16;
+    p.num_tokens = num_tokens;
+    p.num_kv_heads = dims->num_kv_heads;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    cudaError_t e = pa::launch_gather_cache(p, dims->dtype, dims->head_dim, dims->kv_dtype, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "pa_gather_cache launch");
+    return PA_OK;
+}
+
+pa_status pa_rope_frequencies(const pa_rope_config *c, double *inv_freq, double *magnitude) {
+    if (!c || !inv_freq || !magnitude) return fail(PA_ERR_NULL, "config, inv_freq or magnitude is NULL");
+    const int R = c->rotary_dim, n = R / 2;
+    if (R < 2 || R % 2 != 0) return fail(PA_ERR_SHAPE, "rotary_dim %d: must be even and positive", R);
+    if (c->scaling < PA_ROPE_PLAIN || c->scaling > PA_ROPE_YARN) return fail(PA_ERR_SHAPE, "scaling %d is not a pa_rope_scaling", c->scaling);
+    if (!(c->base > 1.0) || !isfinite(c->base)) return fail(PA_ERR_SHAPE, "base must be finite and above 1");
+    if (c->scaling != PA_ROPE_PLAIN && (!(c->factor >= 1.0) || !isfinite(c->factor)))
+        return fail(PA_ERR_SHAPE, "factor must be finite and at least 1");
+    if (c->scaling == PA_ROPE_NTK && R < 4) return fail(PA_ERR_SHAPE, "PA_ROPE_NTK needs rotary_dim >= 4");
+    if (c->scaling >= PA_ROPE_BANDS && (!(c->original_context > 0.0) || !isfinite(c->original_context)))
+        return fail(PA_ERR_SHAPE, "original_context must be finite and positive");
+    if (c->scaling == PA_ROPE_BANDS &&
+        (!(c->low_freq_factor > 0.0) || !(c->high_freq_factor > c->low_freq_factor) || !isfinite(c->high_freq_factor)))
+        return fail(PA_ERR_SHAPE, "0 < low_freq_factor < high_freq_factor is needed");
+    if (c->scaling == PA_ROPE_YARN && (!(c->beta_slow > 0.0) || !(c->beta_fast > c->beta_slow) || !isfinite(c->beta_fast)))
+        return fail(PA_ERR_SHAPE, "0 < beta_slow < beta_fast is needed");
+    constexpr double kTwoPi = 6.283185307179586476925;
+    const double base = c->scaling == PA_ROPE_NTK ? c->base * pow(c->factor, (double)R / (R - 2)) : c->base;
+    // YARN: the (fractional) pair index that turns `turns` times within the original context
+    auto pair_of = [&](double turns) { return R * log(c->original_context / (turns * kTwoPi)) / (2.0 * log(base)); };
+    double first = 0.0, last = 0.0;
+    if (c->scaling == PA_ROPE_YARN) {
+        first = fmax(floor(pair_of(c->beta_fast)), 0.0);
+        last = fmin(ceil(pair_of(c->beta_slow)), R - 1.0);
+        if (last - first < 0.001) last = first + 0.001;
+    }
+    for (int i = 0; i < n; ++i) {
+        const double f = pow(base, -2.0 * i / R);
+        double g = f;
+        if (c->scaling == PA_ROPE_LINEAR) {
+            g = f / c->factor;
+        } else if (c->scaling == PA_ROPE_BANDS) {
+            const double turns = c->original_context * f / kTwoPi;  // C / wavelength
+            const double keep = fmin(fmax((turns - c->low_freq_factor) / (c->high_freq_factor - c->low_freq_factor), 0.0), 1.0);
+            g = (1.0 - keep) * f / c->factor + keep * f;
+        } else if (c->scaling == PA_ROPE_YARN) {
+            const double ramp = fmin(fmax((i - first) / (last - first), 0.0), 1.0);
+            g = ramp * f / c->factor + (1.0 - ramp) * f;
+        }
+        inv_freq[i] = g;
+    }
+    *magnitude = c->scaling == PA_ROPE_YARN ? 0.1 * log(c->factor) + 1.0 : 1.0;
+    return PA_OK;
+}
+
+pa_status pa_rope(void *q_out, const void *q, void *k_out, const void *k, const int64_t *positions,
+                  int32_t num_tokens, const pa_dims *dims, const pa_rope_opts *rope, int64_t q_stride,
+                  int64_t k_stride, void *stream) {
+    if (!dims) return fail(PA_ERR_NULL, "dims is NULL");
+    pa_dims d = *dims;  // no cache: its fields are not looked at
+    d.kv_dtype = 0;
+    d.block_size = 16;
+    d.num_blocks = 1;
+    if (!k) d.num_kv_heads = 1;
+    pa_status st = check_dims(&d, false);
+    if (st == PA_OK) st = check_rope(dims, rope);
+    if (st != PA_OK) return st;
+    if (num_tokens < 0) return fail(PA_ERR_SHAPE, "num_tokens %d < 0", num_tokens);
+    if (q && dims->num_heads <= 0) return fail(PA_ERR_SHAPE, "num_heads %d must be positive", dims->num_heads);
+    if (num_tokens == 0) return PA_OK;
+    if ((!q && !k) || !q != !q_out || !k != !k_out || !positions || !rope->inv_freq)
+        return fail(PA_ERR_NULL, "a required pointer is NULL");
+    pa::RopeParams p{};
+    st = fill_rope(&p, q_out, q, k_out, k, nullptr, positions, num_tokens, dims, rope, q_stride, k_stride, 0);
+    if (st != PA_OK) return st;
+    cudaError_t e = pa::launch_rope(p, dims->dtype, dims->head_dim, -1, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "pa_rope launch");
+    return PA_OK;
+}
+
+pa_status pa_rope_and_cache(void *q_out, const void *q, const void *key, const void *value, void *k_cache,
+                            void *v_cache, const int64_t *slot_mapping, const int64_t *positions, int32_t num_tokens,
+                            const pa_dims *dims, const pa_rope_opts *rope, int64_t q_stride, int64_t k_stride,
+                            int64_t v_stride, float k_scale, float v_scale, void *stream) {
+    pa_status st = check_dims(dims, false);
+    if (st == PA_OK) st = check_rope(dims, rope);
+    if (st != PA_OK) return st;
+    if (!good_scale(k_scale) || !good_scale(v_scale))
+        return fail(PA_ERR_SHAPE, "k_scale and v_scale must be finite and positive");
+    if (!kv_fp8(dims) && (k_scale != 1.f || v_scale != 1.f))
+        return fail(PA_ERR_SHAPE, "k_scale and v_scale must be 1 unless the cache is FP8");
+    if (num_tokens < 0) return fail(PA_ERR_SHAPE, "num_tokens %d < 0", num_tokens);
+    if (q && dims->num_heads <= 0) return fail(PA_ERR_SHAPE, "num_heads %d must be positive", dims->num_heads);
+    if (num_tokens == 0) return PA_OK;
+    if (!q != !q_out || !key || !value || !k_cache || !v_cache || !slot_mapping || !positions || !rope->inv_freq)
+        return fail(PA_ERR_NULL, "a required pointer is NULL");
+    if (!aligned16(k_cache) || !aligned16(v_cache)) return fail(PA_ERR_ALIGN, "caches must be 16-byte aligned");
+    pa::RopeParams p{};
+    st = fill_rope(&p, q_out, q, nullptr, key, value, positions, num_tokens, dims, rope, q_stride, k_stride, v_stride);
+    if (st != PA_OK) return st;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.slots = slot_mapping;
+    p.num_slots = dims->num_blocks * 16;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    cudaError_t e = pa::launch_rope(p, dims->dtype, dims->head_dim, dims->kv_dtype, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "pa_rope_and_cache launch");
     return PA_OK;
 }
 
@@ -442,7 +697,7 @@ pa_status pa_swap_blocks(const void *src_k, const void *src_v, int64_t src_num_b
     const void *bm = device_address(block_mapping);
     if (!sk || !sv || !dk || !dv || !bm)
         return fail(PA_ERR_MEMORY, "a pool or the mapping is not device or page-locked host memory");
-    pa::CacheDims cd{dims->num_kv_heads, dims->head_dim, dims->num_blocks, kv_elem_bytes(dims)};
+    pa::CacheDims cd{dims->num_kv_heads, dims->head_dim, dims->num_blocks, kv_block_bytes(dims)};
     cudaError_t e = pa::launch_swap_blocks(sk, sv, src_num_blocks, const_cast<void *>(dk), const_cast<void *>(dv),
                                            dst_num_blocks, static_cast<const int64_t *>(bm), num_pairs, cd,
                                            static_cast<cudaStream_t>(stream));

@@ -200,7 +200,7 @@ cudaError_t launch_swap_blocks(const void *src_k, const void *src_v, int64_t src
                                int64_t dst_blocks, const int64_t *block_mapping, int32_t num_pairs, const CacheDims &d,
                                cudaStream_t stream) {
     if (num_pairs == 0) return cudaSuccess;
-    const int64_t chunks = (int64_t)d.num_kv_heads * kBlock * d.head_dim * d.elem_bytes / 16;
+    const int64_t chunks = d.block_bytes / 16;
     return launch_pdl(swap_blocks_kernel, dim3(num_pairs, 2), dim3(256), 0, stream, static_cast<const uint4 *>(src_k),
                       static_cast<const uint4 *>(src_v), src_blocks, static_cast<uint4 *>(dst_k),
                       static_cast<uint4 *>(dst_v), dst_blocks, block_mapping, chunks);
@@ -223,7 +223,7 @@ cudaError_t launch_copy_blocks(void *const *k_caches, void *const *v_caches, int
                                const int64_t *block_mapping, int32_t num_pairs, const CacheDims &d,
                                cudaStream_t stream) {
     if (num_pairs == 0 || num_layers == 0) return cudaSuccess;
-    const int64_t chunks = (int64_t)d.num_kv_heads * kBlock * d.head_dim * d.elem_bytes / 16;
+    const int64_t chunks = d.block_bytes / 16;
     for (int l0 = 0; l0 < num_layers; l0 += kCopyLayers) {
         const int nl = num_layers - l0 < kCopyLayers ? num_layers - l0 : kCopyLayers;
         LayerPtrs ptrs = {};

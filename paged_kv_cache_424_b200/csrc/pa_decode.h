@@ -97,11 +97,46 @@ cudaError_t launch_merge_partitions(const DecodeParams &p, int dtype, int head_d
 bool decode_tc_supported(int head_dim, int rows, int64_t num_blocks, int num_kv_heads);
 cudaError_t launch_decode_tc(const DecodeParams &p, int dtype, int rows, bool fp8_cache, cudaStream_t stream);
 
+// Decode over 4-bit caches for `rows` query rows per KV head (8 or 16 >=
+// group * q_len; + merge when max_parts > 1).
+cudaError_t launch_decode_int4(const DecodeParams &p, int dtype, int head_dim, int rows, cudaStream_t stream);
+
+// Rotation of queries and keys, with or without the cache write.
+struct RopeParams {
+    void *q_out;            // [T, H, D], nullptr without queries (num_heads 0)
+    const void *q;          // tokens q_stride elements apart
+    void *k_out;            // [T, Hk, D], nullptr when the keys go to a cache
+    const void *k, *v;      // v only with a cache
+    void *k_cache, *v_cache;
+    const int64_t *slots;      // only with a cache
+    const int64_t *positions;  // may be nullptr when half is 0
+    const double *inv_freq;    // [half]
+    int64_t q_stride, k_stride, v_stride, num_slots;
+    int32_t num_tokens, num_heads, num_kv_heads;
+    int32_t half;  // rotary_dim / 2, 0 = no rotation
+    int32_t interleaved, inverse;
+    double magnitude;
+    float k_scale, v_scale;
+};
+// kv_dtype: the cache's (PA_F16 / PA_BF16: the type of the tokens), or -1 for
+// no cache.
+cudaError_t launch_rope(const RopeParams &p, int dtype, int head_dim, int kv_dtype, cudaStream_t stream);
+
+struct GatherParams {
+    void *key, *value;  // [T, Hk, D]
+    const void *k_cache, *v_cache;
+    const int64_t *slots;
+    int64_t num_slots;
+    int32_t num_tokens, num_kv_heads;
+    float k_scale, v_scale;
+};
+cudaError_t launch_gather_cache(const GatherParams &p, int dtype, int head_dim, int kv_dtype, cudaStream_t stream);
+
 // Cache kernels.
 struct CacheDims {
     int32_t num_kv_heads, head_dim;
     int64_t num_blocks;
-    int32_t elem_bytes;  // 2 for fp16 / bf16, 1 for FP8 E4M3
+    int64_t block_bytes;  // of one block of K or V: all KV heads, 16 tokens
 };
 cudaError_t launch_reshape_and_cache(const void *key, const void *value, void *k_cache, void *v_cache,
                                      const int64_t *slot_mapping, int32_t num_tokens, const CacheDims &d,
