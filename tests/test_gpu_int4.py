@@ -311,6 +311,34 @@ def test_a_poisoned_row_reaches_only_its_readers():
     ref.pool_views(vc)[1].copy_(vt)
 
 
+@pytest.mark.parametrize("group", [1, 4, 8, 16])
+@pytest.mark.parametrize("P", [0, 16])
+def test_nan_queries_and_keys(group, P):
+    """A NaN or infinite query element makes its own row NaN and no other; a
+    NaN key row, even the only token of a sequence or of a partition, makes
+    its KV head's rows of that sequence NaN."""
+    g = gen(26)
+    p = pa()
+    b = batch(g, [1, 17, 200], 2, group, 128, torch.float16)
+    q, kc, vc, tables, lens = b
+    clean = run(*b, 0.09, P=P)
+    bad = q.clone()
+    bad[2, 0, 1, 7] = float("nan")
+    bad[1, 0, group, 100] = float("inf")
+    out = run(bad, kc, vc, tables, lens, 0.09, P=P)
+    hit = torch.zeros(out.shape[:3], dtype=torch.bool, device="cuda")
+    hit[2, 0, 1] = hit[1, 0, group] = True
+    assert bool(out[hit].isnan().all()) and torch.equal(out[~hit], clean[~hit])
+    x = torch.zeros((3, 2, 128), dtype=torch.float16, device="cuda")
+    x[:, 1, 5] = float("nan")
+    slots = torch.stack([tables[0, 0].long() * 16, tables[1, 1].long() * 16, tables[2, 5].long() * 16 + 9])
+    p.pa_reshape_and_cache_int4(x, torch.zeros_like(x), kc, vc.clone(), slots)
+    out = run(q, kc, vc, tables, lens, 0.09, P=P)
+    assert bool(out[:, 0, group:].isnan().all())
+    head0 = run(q, kc, vc, tables, lens, 0.09, P=P)[:, 0, :group]
+    assert bool(head0.isfinite().all())
+
+
 def test_bad_table_entries_and_lengths_are_flagged():
     g = gen(23)
     p = pa()
