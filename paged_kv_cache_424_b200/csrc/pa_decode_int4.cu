@@ -7,8 +7,8 @@
 // so the codes enter both products as integers 0..15 and the scales act on
 // tokens: on a logit after the first product, on a weight before the second.
 //
-// One warp takes 16 tokens (a block) at a time with warp-level matrix
-// instructions:
+// One warp takes 32 tokens (two blocks) at a time with warp-level matrix
+// instructions; for each block
 //   S^T (16 tokens x rows) = U (16 x D) . Q^T       m16n8k32, u8 x s8 -> s32
 //   O^T (D x rows)        += U'^T (D x 16) . W^T    m16n8k16, f16 -> f32
 // with W = p s'.  Unpacking is what bounds such a kernel (logic runs at half
@@ -20,10 +20,12 @@
 //     fp16 elements within 2^4 of it, for bf16 ones within 2^7); a row's two
 //     parts are two columns of the product, so 8 columns hold 4 rows and a
 //     lane gets both parts of one row and adds them as integers.
-//   - V pairs two tokens in a register: two byte permutes bring the tokens'
-//     words together, and w & 0x000f000f or w & 0x00f000f0 is then a pair of
-//     fp16 subnormals u 2^-24 or 16 u 2^-24, exactly, which the matrix units
-//     take as they are (five instructions for eight codes).
+//   - V pairs two tokens in a register: a transposing matrix load of 16-bit
+//     elements brings four codes of one token and the same four dims' codes of
+//     the next into one word, and w & 0x000f000f or w & 0x00f000f0 is then a
+//     pair of fp16 subnormals u 2^-24 or 16 u 2^-24, exactly, which the matrix
+//     units take as they are (with one shift by 8 five instructions for eight
+//     codes).
 // The contraction over dims may run in any order, so a lane's codes are the
 // consecutive bytes that it loads, and Q is laid out to match.  S's
 // accumulator layout (token, row) becomes W's operand layout by movmatrix.
@@ -51,7 +53,7 @@ namespace pa {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kStages = 4;  // per warp: 4 x 2 chunks in flight
+constexpr int kStages = 3;  // per warp, of two blocks each: up to 12 chunks in flight
 constexpr float kTwo24 = 16777216.f;
 constexpr float kMaxWeightScale = 64.f;  // times p <= 2^8 stays inside f16
 
@@ -91,14 +93,24 @@ __device__ __forceinline__ void load_words(uint32_t (&w)[N], const unsigned char
     }
 }
 
+// Four 8x8 matrices of 16-bit elements, each transposed: lane (r, q) gets
+// elements (2q, r) and (2q + 1, r); lane 8 i + k gives the address of row k of
+// matrix i.
+__device__ __forceinline__ void load_matrix4_trans(uint32_t (&w)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
 // Shared memory: per-warp stage rings (reused for the warps' outputs at the
 // end), Q's operands (D / 16 words per lane and tile), the rows' factors, the
 // warps' m and l, the mbarriers.
 struct Int4Layout {
     int main, q_off, fac_off, ml_off, bar_off, bytes;
     __host__ __device__ constexpr Int4Layout(int D, int rows)
-        : main(kWarps * kStages * 2 * int4_chunk_bytes(D) > kWarps * rows * D * 4
-                   ? kWarps * kStages * 2 * int4_chunk_bytes(D)
+        : main(kWarps * kStages * 4 * int4_chunk_bytes(D) > kWarps * rows * D * 4
+                   ? kWarps * kStages * 4 * int4_chunk_bytes(D)
                    : kWarps * rows * D * 4),
           q_off(main), fac_off(q_off + rows / 4 * (D / 16) * 128), ml_off(fac_off + rows * 8),
           bar_off(ml_off + 2 * kWarps * rows * 4), bytes(bar_off + kWarps * kStages * 8) {}
@@ -165,19 +177,19 @@ __device__ __forceinline__ void make_q_tile(uint32_t *dst, float2 *fac, const T 
     }
 }
 
+// CTAs per SM: 4 while the state fits 128 registers.
+__host__ __device__ constexpr int int4_ctas_per_sm(int RT) { return RT == 1 ? 4 : RT == 2 ? 3 : 2; }
+
 // RT: tiles of 4 query rows (1, 2 or 4).  Lane (r, q) = (lane / 4, lane % 4)
 // holds
-//   of S: tokens tau(r) and 8 + tau(r), query row 4 n + q of each tile n;
-//   of K: D / 4 dims from D / 4 q of those two tokens;
-//   of V: D / 8 dims from D / 8 r of tokens tau(2q), tau(2q + 1) and those + 8;
+//   of S: tokens r and 8 + r of each block, query row 4 n + q of each tile n;
+//   of K: D / 4 dims from D / 4 q of those tokens;
+//   of V: dims 32 g + 4 r .. + 3 of tokens 2q, 2q + 1, 8 + 2q and 9 + 2q;
 //   of O: those dims, query rows 4 n + q.
-// tau swaps the tokens of every other pair, so that the V rows of one load
-// fall on both halves of the banks (2-way instead of 4-way conflicts).
 template <typename T, int D, int RT, bool kMasked>
-__global__ void __launch_bounds__(kWarps * 32) decode_int4_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(kWarps * 32, int4_ctas_per_sm(RT)) decode_int4_kernel(const DecodeParams p) {
     using E = Elem<T>;
     constexpr int KW = D / 32;   // words of K per lane and token
-    constexpr int VW = D / 64;   // words of V per lane and token
     constexpr int MT = D / 16;   // tiles of 16 dims
     constexpr int RW = 4 * RT;   // query rows
     constexpr int NP = RT == 1 ? 1 : RT / 2;  // column tiles of the second product
@@ -195,16 +207,17 @@ __global__ void __launch_bounds__(kWarps * 32) decode_int4_kernel(const DecodePa
     const int s = scheduled_seq(p, blockIdx.z, part == 0 && kvh == 0 && tid == 0);
     const SeqSplit sp = s < 0 ? SeqSplit{0, 0, 0, 0} : seq_split(p, s, part == 0 && kvh == 0 && tid == 0);
     const int L = sp.L;
-    // this warp's blocks: every kWarps-th of the partition
+    // this warp's pairs of blocks: every kWarps-th of the partition
     const int b0 = sp.bfirst + part * p.part_blocks;
     const int b1 = min(b0 + p.part_blocks, sp.nblk);
-    const int nw = part < sp.nparts ? (b1 - b0 - warp + kWarps - 1) / kWarps : 0;  // may be <= 0
-    const int32_t *table = p.block_tables + (int64_t)s * p.max_blocks_per_seq + b0 + warp;
-    auto window = [&](int w) -> int32_t {  // entries 32 w .. 32 w + 31, one per lane
-        const int j = 32 * w + lane;
-        return j < nw ? (int32_t)checked_block(p, table[kWarps * j]) : 0;
+    const int np = part < sp.nparts ? ((b1 - b0 + 1) / 2 - warp + kWarps - 1) / kWarps : 0;  // may be <= 0
+    const int tend = min(L, b1 * kBlock);                                                    // this CTA's last token + 1
+    auto block_of = [&](int e) -> int { return b0 + 2 * (warp + kWarps * (e >> 1)) + (e & 1); };
+    auto window = [&](int w) -> int32_t {  // the blocks of pairs 16 w .. 16 w + 15, one per lane; -1 past the end
+        const int b = block_of(32 * w + lane);
+        return b < b1 && 16 * w < np ? (int32_t)checked_block(p, p.block_tables[(int64_t)s * p.max_blocks_per_seq + b]) : -1;
     };
-    int32_t cur = window(0), next = nw > 32 ? window(1) : 0;
+    int32_t cur = window(0), next = window(1);
     uint64_t *wbar = bars + warp * kStages;
     if (lane == 0) {
         for (int i = 0; i < kStages; ++i) mbar_init(&wbar[i], 1);
@@ -223,25 +236,27 @@ __global__ void __launch_bounds__(kWarps * 32) decode_int4_kernel(const DecodePa
         for (int i = tid; i < rows * D; i += blockDim.x) out[row_of(i / D) * D + i % D] = E::from_float(0.f);
         return;
     }
-    // the loads of block j (all lanes, j in ascending order): lane 0 K, lane 1 V
-    unsigned char *ring = smem + warp * kStages * 2 * kChunk;
-    const unsigned char *pool = reinterpret_cast<const unsigned char *>(lane == 0 ? p.k_cache : p.v_cache) + (int64_t)kvh * kChunk;
+    // the loads of pair j (all lanes, j in ascending order): lane i brings
+    // chunk i of the stage (K and V of its first block, K and V of its second)
+    unsigned char *ring = smem + warp * kStages * 4 * kChunk;
+    const unsigned char *pool = reinterpret_cast<const unsigned char *>((lane & 1) ? p.v_cache : p.k_cache) + (int64_t)kvh * kChunk;
     const uint32_t block_bytes = (uint32_t)(p.num_kv_heads * kChunk);
-    auto issue = [&](int j) {
-        if ((j & 31) == 0 && j > 0) {
+    auto issue = [&](int j, int st) {
+        if ((j & 15) == 0 && j > 0) {
             cur = next;
-            next = 32 * (j / 32 + 1) < nw ? window(j / 32 + 1) : 0;
+            next = window(j / 16 + 1);
         }
-        const uint32_t phys = (uint32_t)__shfl_sync(0xffffffffu, cur, j & 31);
-        if (lane < 2) {
-            uint64_t *bar = &wbar[j % kStages];
-            if (lane == 0) mbar_arrive_expect_tx(bar, 2 * kChunk);
-            __syncwarp(3u);
-            bulk_g2s(ring + (j % kStages) * 2 * kChunk + lane * kChunk, pool + (uint64_t)phys * block_bytes, kChunk, bar);
+        const int32_t phys = __shfl_sync(0xffffffffu, cur, ((j & 15) << 1) + ((lane >> 1) & 1));
+        const bool both = __shfl_sync(0xffffffffu, phys, 2) >= 0;
+        if (lane < 4) {
+            if (lane == 0) mbar_arrive_expect_tx(&wbar[st], both ? 4 * kChunk : 2 * kChunk);
+            __syncwarp(15u);
+            if (phys >= 0)
+                bulk_g2s(ring + (st * 4 + lane) * kChunk, pool + (uint64_t)(uint32_t)phys * block_bytes, kChunk, &wbar[st]);
         }
     };
     __syncwarp();  // the barriers are initialised
-    for (int j = 0; j < kStages && j < nw; ++j) issue(j);
+    for (int j = 0; j < kStages && j < np; ++j) issue(j, j);
 
     // ---- query rows ---------------------------------------------------------
     uint32_t *q_s = reinterpret_cast<uint32_t *>(smem + Lay.q_off);
@@ -285,80 +300,106 @@ __global__ void __launch_bounds__(kWarps * 32) decode_int4_kernel(const DecodePa
         for (int t = 0; t < MT; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[n][t][i] = 0.f;
-    const int tau = r ^ ((r >> 1) & 1), tv0 = (2 * q) ^ (q & 1), tv1 = tv0 ^ 1;
+    const uint32_t ring_addr = smem_addr(ring);
+    const int k_lane = r * (D / 2) + q * (D / 8);
+    const int v_lane = D == 128 ? (lane & 7) * 64 + (lane >> 3) * 16 : ((lane & 7) + 8 * (lane >> 4)) * 32 + ((lane >> 3) & 1) * 16;
     bool ok = true;
-    int j = 0;
+    int j = 0, st = 0;
+    uint32_t parity = 0;
 #pragma unroll 1
-    for (; j < nw; ++j) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&wbar[j % kStages], (j / kStages) & 1))) {
+    for (; j < np; ++j) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&wbar[st], parity))) {
             ok = false;
             break;
         }
-        const unsigned char *ks = ring + (j % kStages) * 2 * kChunk, *vs = ks + kChunk;
-        uint32_t k0[KW], k1[KW], va[VW], vb[VW], vd[VW], ve[VW];
-        load_words<KW>(k0, ks + tau * (D / 2) + q * (D / 8));
-        load_words<KW>(k1, ks + (8 + tau) * (D / 2) + q * (D / 8));
-        load_words<VW>(va, vs + tv0 * (D / 2) + r * (D / 16));
-        load_words<VW>(vb, vs + tv1 * (D / 2) + r * (D / 16));
-        load_words<VW>(vd, vs + (8 + tv0) * (D / 2) + r * (D / 16));
-        load_words<VW>(ve, vs + (8 + tv1) * (D / 2) + r * (D / 16));
-        float2 ke[2], ce[2];  // (scale, low) of the lane's two tokens in K and V
+        const unsigned char *stage = ring + st * 4 * kChunk;
+        float2 ke[4], ce[4];  // (scale, low) of the lane's tokens r, 8 + r, 16 + r, 24 + r in K and V
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            ke[i] = int4_ends(*reinterpret_cast<const uint32_t *>(ks + int4_ends_offset(D) + 4 * (8 * i + tau)));
-            ce[i] = int4_ends(*reinterpret_cast<const uint32_t *>(vs + int4_ends_offset(D) + 4 * (8 * i + tau)));
+        for (int i = 0; i < 4; ++i) {
+            const unsigned char *e = stage + 2 * (i >> 1) * kChunk + int4_ends_offset(D) + 4 * (8 * (i & 1) + r);
+            ke[i] = int4_ends(*reinterpret_cast<const uint32_t *>(e));
+            ce[i] = int4_ends(*reinterpret_cast<const uint32_t *>(e + kChunk));
+        }
+        // S^T = U Q^T: even dims' codes, and odd dims' codes times 16
+        float raw[RT][4], x[RT][4];  // T = 16 q . u of the four tokens, the logits minus m
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            uint32_t k0[KW], k1[KW];
+            load_words<KW>(k0, stage + 2 * b * kChunk + k_lane);
+            load_words<KW>(k1, stage + 2 * b * kChunk + k_lane + 8 * (D / 2));
+#pragma unroll
+            for (int n = 0; n < RT; ++n) {
+                int ev[4] = {0, 0, 0, 0}, od[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int w = 0; w < KW; w += 2) {
+                    mma_u8s8(ev, k0[w] & 0x0f0f0f0fu, k1[w] & 0x0f0f0f0fu, k0[w + 1] & 0x0f0f0f0fu,
+                             k1[w + 1] & 0x0f0f0f0fu, qb[n][2 * w], qb[n][2 * w + 2]);
+                    mma_u8s8(od, k0[w] & 0xf0f0f0f0u, k1[w] & 0xf0f0f0f0u, k0[w + 1] & 0xf0f0f0f0u,
+                             k1[w + 1] & 0xf0f0f0f0u, qb[n][2 * w + 1], qb[n][2 * w + 3]);
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    raw[n][2 * b + i] = (float)((ev[2 * i] * 128 + ev[2 * i + 1]) * 16 + (od[2 * i] * 128 + od[2 * i + 1]));
+            }
+        }
+        // V's codes: pairs of tokens, four dims per word
+        uint32_t vw[2][D / 32][2];  // [block][group of 32 dims][tokens 2q.., 8 + 2q..]
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const uint32_t at = ring_addr + (st * 4 + 2 * b + 1) * kChunk + v_lane;
+            uint32_t w[4];
+            load_matrix4_trans(w, at);
+            if constexpr (D == 128) {
+                uint32_t h[4];
+                load_matrix4_trans(h, at + 8 * 64);
+#pragma unroll
+                for (int g = 0; g < 4; ++g) vw[b][g][0] = w[g], vw[b][g][1] = h[g];
+            } else {
+                vw[b][0][0] = w[0], vw[b][1][0] = w[1], vw[b][0][1] = w[2], vw[b][1][1] = w[3];
+            }
         }
         __syncwarp();
-        if (j + kStages < nw) {  // the block is in registers: its stage may be filled again
+        if (j + kStages < np) {  // the pair is in registers: its stage may be filled again
             fence_proxy_async_smem();
-            issue(j + kStages);
+            issue(j + kStages, st);
+        }
+        if (++st == kStages) {
+            st = 0;
+            parity ^= 1;
         }
 
-        // S^T = U Q^T: even dims' codes, and odd dims' codes times 16
-        float x[RT][2];  // T = 16 q . u of the two tokens, then the logits minus m
-#pragma unroll
-        for (int n = 0; n < RT; ++n) {
-            int ev[4] = {0, 0, 0, 0}, od[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (int w = 0; w < KW; w += 2) {
-                mma_u8s8(ev, k0[w] & 0x0f0f0f0fu, k1[w] & 0x0f0f0f0fu, k0[w + 1] & 0x0f0f0f0fu, k1[w + 1] & 0x0f0f0f0fu,
-                         qb[n][2 * w], qb[n][2 * w + 2]);
-                mma_u8s8(od, k0[w] & 0xf0f0f0f0u, k1[w] & 0xf0f0f0f0u, k0[w + 1] & 0xf0f0f0f0u, k1[w + 1] & 0xf0f0f0f0u,
-                         qb[n][2 * w + 1], qb[n][2 * w + 3]);
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                x[n][i] = (float)((ev[2 * i] * 128 + ev[2 * i + 1]) * 16 + (od[2 * i] * 128 + od[2 * i + 1]));
-        }
-        const int base = (b0 + warp + kWarps * j) * kBlock;
-        const bool whole = !kMasked && base + kBlock <= L;
-        bool dead[RT][2];
+        const int base = (b0 + 2 * (warp + kWarps * j)) * kBlock + r;  // the lane's first token
+        const bool whole = !kMasked && base - r + 2 * kBlock <= tend;
+        bool dead[RT][4];
         if (!whole) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int tok = base + 8 * i + tau;
+            for (int i = 0; i < 4; ++i) {
+                const int tok = base + 8 * i;
                 // rows that no query sees may hold anything
-                if (tok >= L || (kMasked && tok < first)) ce[i] = make_float2(0.f, 0.f);
+                if (tok >= tend || (kMasked && tok < first)) ce[i] = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int n = 0; n < RT; ++n) dead[n][i] = kMasked ? tok < lo[n] || tok > hi[n] : tok >= L;
+                for (int n = 0; n < RT; ++n) dead[n][i] = tok >= tend || (kMasked && (tok < lo[n] || tok > hi[n]));
             }
         }
-        float raw[RT][2];
+        auto logits = [&](int n) {  // +inf before the first maximum
 #pragma unroll
-        for (int n = 0; n < RT; ++n)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                raw[n][i] = x[n][i];
-                x[n][i] = fmaf(ke[i].x * fac[n], raw[n][i], fmaf(ke[i].y, off_q[n], -m[n]));  // +inf before the first max
+            for (int i = 0; i < 4; ++i) {
+                x[n][i] = fmaf(ke[i].x * fac[n], raw[n][i], fmaf(ke[i].y, off_q[n], -m[n]));
                 if (!whole && dead[n][i]) x[n][i] = -INFINITY;
             }
+        };
         // running maxima, raised only when a logit beats one by 2^8 or a V
         // scale its power of two (NaN takes this way too)
-        bool exceed = fmaxf(fabsf(ce[0].x), fabsf(ce[1].x)) > limit;
+        const float big4 = fmaxf(fmaxf(fabsf(ce[0].x), fabsf(ce[1].x)), fmaxf(fabsf(ce[2].x), fabsf(ce[3].x)));
+        bool exceed = big4 > limit;
 #pragma unroll
-        for (int n = 0; n < RT; ++n) exceed = exceed || !(x[n][0] <= kLazyMax) || !(x[n][1] <= kLazyMax);
+        for (int n = 0; n < RT; ++n) {
+            logits(n);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) exceed = exceed || !(x[n][i] <= kLazyMax);
+        }
         if (__any_sync(0xffffffffu, exceed)) {
-            float big = fmaxf(fabsf(ce[0].x), fabsf(ce[1].x));
+            float big = big4;
 #pragma unroll
             for (int o = 16; o > 2; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
             float turn = 1.f;  // new power of two over the old one
@@ -372,12 +413,12 @@ __global__ void __launch_bounds__(kWarps * 32) decode_int4_kernel(const DecodePa
             }
 #pragma unroll
             for (int n = 0; n < RT; ++n) {
-                float v[2], bm = -INFINITY;
+                float bm = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    v[i] = fmaf(ke[i].x * fac[n], raw[n][i], ke[i].y * off_q[n]);
-                    if (!whole && dead[n][i]) v[i] = -INFINITY;
-                    bm = fmaxf(bm, v[i] != v[i] ? 0.f : v[i]);  // a NaN row gets a finite maximum and NaN sums
+                for (int i = 0; i < 4; ++i) {
+                    float v = fmaf(ke[i].x * fac[n], raw[n][i], ke[i].y * off_q[n]);
+                    if (!whole && dead[n][i]) v = -INFINITY;
+                    bm = fmaxf(bm, v != v ? 0.f : v);  // a NaN row gets a finite maximum and NaN sums
                 }
 #pragma unroll
                 for (int o = 16; o > 2; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, o));
@@ -400,17 +441,13 @@ __global__ void __launch_bounds__(kWarps * 32) decode_int4_kernel(const DecodePa
                         acc[n / 2][t][2 + (n & 1)] *= alpha;
                     }
                 }
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    x[n][i] = fmaf(ke[i].x * fac[n], raw[n][i], fmaf(ke[i].y, off_q[n], -m[n]));
-                    if (!whole && dead[n][i]) x[n][i] = -INFINITY;
-                }
+                logits(n);
             }
         }
         // weights, turned into the second product's operand
-        uint32_t wb[NP][2];
+        uint32_t wb[NP][4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
             const float sv = ce[i].x * cv;
             float w[RT];
 #pragma unroll
@@ -436,20 +473,18 @@ __global__ void __launch_bounds__(kWarps * 32) decode_int4_kernel(const DecodePa
                 }
             }
         }
-        // O^T += U'^T W^T: tile 4 w + 2 v + u holds dims 8 w + 4 v + 2 u (and + 1, times 16)
+        // O^T += U'^T W^T: tile 2 g + u holds dims 32 g + 4 r + 2 u (and + 1, times 16)
 #pragma unroll
-        for (int w = 0; w < VW; ++w)
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                const uint32_t a = __byte_perm(va[w], vb[w], v ? 0x7632 : 0x5410);
-                const uint32_t b = __byte_perm(vd[w], ve[w], v ? 0x7632 : 0x5410);
-                const uint32_t a8 = a >> 8, b8 = b >> 8;
+            for (int g = 0; g < D / 32; ++g) {
+                const uint32_t a = vw[b][g][0], c = vw[b][g][1], a8 = a >> 8, c8 = c >> 8;
 #pragma unroll
                 for (int n = 0; n < NP; ++n) {
-                    mma_f16(acc[n][4 * w + 2 * v], a & 0x000f000fu, a & 0x00f000f0u, b & 0x000f000fu, b & 0x00f000f0u,
-                            wb[n][0], wb[n][1]);
-                    mma_f16(acc[n][4 * w + 2 * v + 1], a8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x000f000fu,
-                            b8 & 0x00f000f0u, wb[n][0], wb[n][1]);
+                    mma_f16(acc[n][2 * g], a & 0x000f000fu, a & 0x00f000f0u, c & 0x000f000fu, c & 0x00f000f0u,
+                            wb[n][2 * b], wb[n][2 * b + 1]);
+                    mma_f16(acc[n][2 * g + 1], a8 & 0x000f000fu, a8 & 0x00f000f0u, c8 & 0x000f000fu, c8 & 0x00f000f0u,
+                            wb[n][2 * b], wb[n][2 * b + 1]);
                 }
             }
     }
@@ -457,7 +492,7 @@ __global__ void __launch_bounds__(kWarps * 32) decode_int4_kernel(const DecodePa
         // A copy never completed (the error word is set): every copy still out
         // gets one more bounded chance to land before the CTA exits.
         if (lane == 0)
-            for (int jj = j; jj < j + kStages && jj < nw; ++jj)
+            for (int jj = j; jj < j + kStages && jj < np; ++jj)
                 mbar_wait(&wbar[jj % kStages], (jj / kStages) & 1, 200000000ll);
         atomicOr(&fail_s, 1);
     }
@@ -479,12 +514,17 @@ __global__ void __launch_bounds__(kWarps * 32) decode_int4_kernel(const DecodePa
         }
         if (h >= rows) continue;
         const float add = kSplit ? z[n] : fmaf(7.5f * zc[n], back, z[n]);
-        float *dst = red_acc + (warp * RW + h) * D + r * (D / 8);
+        float *dst = red_acc + (warp * RW + h) * D + 4 * r;
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            const float *c = acc[n / 2][t];
-            const float a = kSplit ? c[0] + c[1] : c[n & 1], b = kSplit ? c[2] + c[3] : c[2 + (n & 1)];
-            *reinterpret_cast<float2 *>(dst + 2 * t) = make_float2(fmaf(a * kTwo24, back, add), fmaf(b * (kTwo24 / 16.f), back, add));
+        for (int g = 0; g < D / 32; ++g) {
+            float o[4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const float *c = acc[n / 2][2 * g + u];
+                o[2 * u] = fmaf((kSplit ? c[0] + c[1] : c[n & 1]) * kTwo24, back, add);
+                o[2 * u + 1] = fmaf((kSplit ? c[2] + c[3] : c[2 + (n & 1)]) * (kTwo24 / 16.f), back, add);
+            }
+            *reinterpret_cast<float4 *>(dst + 32 * g) = make_float4(o[0], o[1], o[2], o[3]);
         }
         if (r == 0) {
             red_m[warp * RW + h] = m[n];
