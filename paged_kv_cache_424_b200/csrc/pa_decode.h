@@ -97,9 +97,15 @@ cudaError_t launch_merge_partitions(const DecodeParams &p, int dtype, int head_d
 bool decode_tc_supported(int head_dim, int rows, int64_t num_blocks, int num_kv_heads);
 cudaError_t launch_decode_tc(const DecodeParams &p, int dtype, int rows, bool fp8_cache, cudaStream_t stream);
 
-// Decode over 4-bit caches for `rows` query rows per KV head (8 or 16 >=
-// group * q_len; + merge when max_parts > 1).
-cudaError_t launch_decode_int4(const DecodeParams &p, int dtype, int head_dim, int rows, cudaStream_t stream);
+// Decode over 4-bit caches for `rows` >= group * q_len query rows per KV head.
+// With `starts` (int64 [num_seqs + 1] in the workspace) the contexts are cut
+// into equal shares of `ctas` CTAs (decode_int4_ctas(rows, SMs); ws_o and ws_lse
+// hold two rows sets per warp, kInt4Warps warps per CTA); without, into the
+// partitions of p.
+constexpr int kInt4Warps = 4;
+int decode_int4_ctas(int rows, int sms);
+cudaError_t launch_decode_int4(const DecodeParams &p, int dtype, int head_dim, int rows, int64_t *starts, int ctas,
+                               cudaStream_t stream);
 
 // Rotation of queries and keys, with or without the cache write.
 struct RopeParams {

@@ -29,7 +29,8 @@
 // The contraction over dims may run in any order, so a lane's codes are the
 // consecutive bytes that it loads, and Q is laid out to match.  S's
 // accumulator layout (token, row) becomes W's operand layout by movmatrix.
-// No shared-memory round trip, no barrier in the loop and no tensor memory:
+// A warp needs no other warp: no shared-memory round trip, no barrier in the
+// loop and no tensor memory:
 // with 5th-generation MMAs the codes would be written back to shared memory,
 // widened, before the MMA could read them, and each 128-token chunk would
 // wait for S to come back from TMEM and for P to go in; the FP8 kernel that is
@@ -39,7 +40,16 @@
 // A code is 0..15 and not -8..7, so a weight's rounding error would count 7.5
 // codes where a centred code's would cancel.  With up to 4 rows the rounding's
 // remainder takes the second column of each row (hi + lo: 22 bits); with more,
-// the remainders are summed and given back at the middle code 7.5.
+// the weights' sum before and after the rounding (the latter by one more MMA
+// against ones) says what it took, which is given back at the middle code 7.5.
+//
+// Two kernels share the warp's work.  decode_int4_kernel: CTA = (partition, KV
+// head, sequence), the warps take every 4th pair of blocks and merge their
+// states in shared memory; used for partitions that the caller sized and for
+// short contexts.  decode_int4_balanced_kernel: one wave of resident warps,
+// each taking an equal share of all (sequence, KV head, block) in their flat
+// order, whatever the lengths; a piece of a context that its warp does not
+// hold whole goes to the workspace, and merge_int4_kernel joins the pieces.
 #include <cfloat>
 #include <type_traits>
 
@@ -52,7 +62,7 @@ namespace pa {
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = kInt4Warps;
 constexpr int kStages = 3;  // per warp, of two blocks each: up to 12 chunks in flight
 constexpr float kTwo24 = 16777216.f;
 constexpr float kMaxWeightScale = 64.f;  // times p <= 2^8 stays inside f16
@@ -103,216 +113,130 @@ __device__ __forceinline__ void load_matrix4_trans(uint32_t (&w)[4], uint32_t ad
                  : "memory");
 }
 
-// Shared memory: per-warp stage rings (reused for the warps' outputs at the
-// end), Q's operands (D / 16 words per lane and tile), the rows' factors, the
-// warps' m and l, the mbarriers.
-struct Int4Layout {
-    int main, q_off, fac_off, ml_off, bar_off, bytes;
-    __host__ __device__ constexpr Int4Layout(int D, int rows)
-        : main(kWarps * kStages * 4 * int4_chunk_bytes(D) > kWarps * rows * D * 4
-                   ? kWarps * kStages * 4 * int4_chunk_bytes(D)
-                   : kWarps * rows * D * 4),
-          q_off(main), fac_off(q_off + rows / 4 * (D / 16) * 128), ml_off(fac_off + rows * 8),
-          bar_off(ml_off + 2 * kWarps * rows * 4), bytes(bar_off + kWarps * kStages * 8) {}
-};
-
-// Q's operands of row tile n (rows 4 n .. 4 n + 3), by one warp: lane (r, q)
-// makes part r & 1 of row 4 n + r / 2, dims D / 4 q ..: per word w of K (8
-// dims) the 4 even dims' parts, and the 4 odd dims'.
-template <typename T, int D>
-__device__ __forceinline__ void make_q_tile(uint32_t *dst, float2 *fac, const T *src, bool real, float scale_log2,
-                                            int row, int lane) {
-    using E = Elem<T>;
-    constexpr int KW = D / 32;
-    const int r = lane >> 2, q = lane & 3;
-    float y[D / 4];
-#pragma unroll
-    for (int i = 0; i < KW; ++i) {
-        const uint4 w = real ? *reinterpret_cast<const uint4 *>(src + q * (D / 4) + 8 * i) : make_uint4(0, 0, 0, 0);
-        const float2 a = E::to_float2(w.x), b = E::to_float2(w.y), c = E::to_float2(w.z), d = E::to_float2(w.w);
-        y[8 * i] = a.x, y[8 * i + 1] = a.y, y[8 * i + 2] = b.x, y[8 * i + 3] = b.y;
-        y[8 * i + 4] = c.x, y[8 * i + 5] = c.y, y[8 * i + 6] = d.x, y[8 * i + 7] = d.y;
-    }
-    float mx = 0.f;
-    int fine = 1;
-#pragma unroll
-    for (int i = 0; i < D / 4; ++i) {
-        mx = fmaxf(mx, fabsf(y[i]));
-        fine &= fabsf(y[i]) <= FLT_MAX;
-    }
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        fine &= __shfl_xor_sync(0xffffffffu, fine, o);
-    }
-    int e = 0;
-    if (mx > 0.f && fine) {
-        (void)frexpf(mx, &e);  // mx in [2^(e-1), 2^e)
-        e = min(14 - e, 120);  // mx 2^e in [2^13, 2^14)
-    }
-    const float up = ldexpf(1.f, e);
-    int sum = 0;
-    uint32_t part[2 * KW];
-#pragma unroll
-    for (int w = 0; w < KW; ++w)
-#pragma unroll
-        for (int odd = 0; odd < 2; ++odd) {
-            uint32_t bytes = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int v = fine ? min(__float2int_rn(y[8 * w + 2 * i + odd] * up), 16383) : 0;
-                sum += v;
-                bytes |= (uint32_t)(((r & 1) ? v & 127 : v >> 7) & 255) << (8 * i);
-            }
-            part[2 * w + odd] = bytes;
-        }
-    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-#pragma unroll
-    for (int k = 0; k < 2 * KW; ++k) dst[k * 32 + lane] = part[k];
-    // logit = s T f + l o with T = 16 q . u (as integers): f = c 2^-e / 16, o = c sum(q)
-    if (q == 0 && (r & 1) == 0) {
-        const float f = ldexpf(scale_log2, -e);
-        fac[row] = fine ? make_float2(f * 0.0625f, (float)sum * f) : make_float2(NAN, NAN);
-    }
+// max of three, NaN if one of them is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
-// CTAs per SM: 4 while the state fits 128 registers.
-__host__ __device__ constexpr int int4_ctas_per_sm(int RT) { return RT == 1 ? 4 : RT == 2 ? 3 : 2; }
+// One warp's ring of stages (four chunks each: K and V of two blocks).
+template <int D>
+struct Int4Ring {
+    unsigned char *base;
+    uint64_t *bars;  // [kStages]
+    int st;          // stage of the next pair to consume
+    uint32_t parity;
+};
 
-// RT: tiles of 4 query rows (1, 2 or 4).  Lane (r, q) = (lane / 4, lane % 4)
-// holds
+// The blocks of one (sequence, KV head) that a warp works on: pair j is table
+// entries first + 2 stride j and the one after it, those below `end`.
+struct Int4Span {
+    int s, kvh, L, first, stride, end, pairs;
+};
+
+// A warp's state for RT tiles of 4 query rows (RT = 1, 2 or 4).  Lane (r, q) =
+// (lane / 4, lane % 4) holds
 //   of S: tokens r and 8 + r of each block, query row 4 n + q of each tile n;
 //   of K: D / 4 dims from D / 4 q of those tokens;
 //   of V: dims 32 g + 4 r .. + 3 of tokens 2q, 2q + 1, 8 + 2q and 9 + 2q;
 //   of O: those dims, query rows 4 n + q.
 template <typename T, int D, int RT, bool kMasked>
-__global__ void __launch_bounds__(kWarps * 32, int4_ctas_per_sm(RT)) decode_int4_kernel(const DecodeParams p) {
+struct Int4Warp {
     using E = Elem<T>;
-    constexpr int KW = D / 32;   // words of K per lane and token
-    constexpr int MT = D / 16;   // tiles of 16 dims
-    constexpr int RW = 4 * RT;   // query rows
-    constexpr int NP = RT == 1 ? 1 : RT / 2;  // column tiles of the second product
-    constexpr bool kSplit = RT == 1;          // weights as two f16 parts
-    constexpr int kChunk = int4_chunk_bytes(D);
-    constexpr Int4Layout Lay(D, RW);
-    extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ int fail_s;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Lay.bar_off);
-    const int part = blockIdx.x, kvh = blockIdx.y;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, q = lane & 3;
-    pdl_launch_dependents();
-    // Order, lengths and tables are read before the wait for the kernel in
-    // front (no kernel of this library writes them), q and the caches after.
-    const int s = scheduled_seq(p, blockIdx.z, part == 0 && kvh == 0 && tid == 0);
-    const SeqSplit sp = s < 0 ? SeqSplit{0, 0, 0, 0} : seq_split(p, s, part == 0 && kvh == 0 && tid == 0);
-    const int L = sp.L;
-    // this warp's pairs of blocks: every kWarps-th of the partition
-    const int b0 = sp.bfirst + part * p.part_blocks;
-    const int b1 = min(b0 + p.part_blocks, sp.nblk);
-    const int np = part < sp.nparts ? ((b1 - b0 + 1) / 2 - warp + kWarps - 1) / kWarps : 0;  // may be <= 0
-    const int tend = min(L, b1 * kBlock);                                                    // this CTA's last token + 1
-    auto block_of = [&](int e) -> int { return b0 + 2 * (warp + kWarps * (e >> 1)) + (e & 1); };
-    auto window = [&](int w) -> int32_t {  // the blocks of pairs 16 w .. 16 w + 15, one per lane; -1 past the end
-        const int b = block_of(32 * w + lane);
-        return b < b1 && 16 * w < np ? (int32_t)checked_block(p, p.block_tables[(int64_t)s * p.max_blocks_per_seq + b]) : -1;
-    };
-    int32_t cur = window(0), next = window(1);
-    uint64_t *wbar = bars + warp * kStages;
-    if (lane == 0) {
-        for (int i = 0; i < kStages; ++i) mbar_init(&wbar[i], 1);
-        fence_mbar_init();
-    }
-    if (tid == 0) fail_s = 0;
-    pdl_wait();
-    if (part >= sp.nparts) return;  // s < 0 too
-    const int rows = p.group * p.q_len;
-    T *out = reinterpret_cast<T *>(p.out);
-    auto row_of = [&](int h) -> int64_t {
-        if constexpr (kMasked) return query_row(p, s, kvh, h);
-        return (int64_t)s * p.num_heads + kvh * p.group + h;
-    };
-    if (L == 0) {
-        for (int i = tid; i < rows * D; i += blockDim.x) out[row_of(i / D) * D + i % D] = E::from_float(0.f);
-        return;
-    }
-    // the loads of pair j (all lanes, j in ascending order): lane i brings
-    // chunk i of the stage (K and V of its first block, K and V of its second)
-    unsigned char *ring = smem + warp * kStages * 4 * kChunk;
-    const unsigned char *pool = reinterpret_cast<const unsigned char *>((lane & 1) ? p.v_cache : p.k_cache) + (int64_t)kvh * kChunk;
-    const uint32_t block_bytes = (uint32_t)(p.num_kv_heads * kChunk);
-    auto issue = [&](int j, int st) {
-        if ((j & 15) == 0 && j > 0) {
-            cur = next;
-            next = window(j / 16 + 1);
-        }
-        const int32_t phys = __shfl_sync(0xffffffffu, cur, ((j & 15) << 1) + ((lane >> 1) & 1));
-        const bool both = __shfl_sync(0xffffffffu, phys, 2) >= 0;
-        if (lane < 4) {
-            if (lane == 0) mbar_arrive_expect_tx(&wbar[st], both ? 4 * kChunk : 2 * kChunk);
-            __syncwarp(15u);
-            if (phys >= 0)
-                bulk_g2s(ring + (st * 4 + lane) * kChunk, pool + (uint64_t)(uint32_t)phys * block_bytes, kChunk, &wbar[st]);
-        }
-    };
-    __syncwarp();  // the barriers are initialised
-    for (int j = 0; j < kStages && j < np; ++j) issue(j, j);
+    static constexpr int KW = D / 32;                    // words of K per lane and token
+    static constexpr int MT = D / 16;                    // tiles of 16 dims
+    static constexpr int NP = RT == 1 ? 1 : RT / 2;      // column tiles of the second product
+    static constexpr bool kSplit = RT == 1;              // weights as two f16 parts
+    static constexpr bool kOneSum = RT > 1;              // odd dims' codes shifted, one accumulator
+    static constexpr int kChunk = int4_chunk_bytes(D);
 
-    // ---- query rows ---------------------------------------------------------
-    uint32_t *q_s = reinterpret_cast<uint32_t *>(smem + Lay.q_off);
-    float2 *fac_s = reinterpret_cast<float2 *>(smem + Lay.fac_off);
-    if (warp < RT) {
-        const int h = 4 * warp + (r >> 1);
-        make_q_tile<T, D>(q_s + warp * (D / 16) * 32, fac_s, reinterpret_cast<const T *>(p.q) + row_of(h < rows ? h : 0) * D,
-                          h < rows, p.scale_log2, h, lane);
-    }
-    __syncthreads();
     uint32_t qb[RT][2 * KW];
     float fac[RT], off_q[RT];
+    int lo[RT], hi[RT];   // attended positions
+    int lo_any, lo_all, hi_all;  // seen by some row from lo_any; by all rows in [lo_all, hi_all]
+    float m[RT], l[RT], z[RT], zw[RT], acc[NP][MT][4], accw[NP][4];
+    float cv;     // power of two the V scales are multiplied by (warp-uniform)
+    float limit;  // V scale above which it is chosen anew
+
+    // Query rows of (s, kvh): q = (128 hi + lo) 2^-e; this lane makes part r & 1 of
+    // row 4 n + r / 2, the dims it holds of K, per word (8 dims) the even dims'
+    // bytes and the odd dims'.  logit = s T fac + low off with T = 16 q . u (u
+    // alone with kOneSum: q . u) as an integer.
+    __device__ __forceinline__ void start(const DecodeParams &p, int s, int kvh, int L, int lane) {
+        const int r = lane >> 2, q = lane & 3, rows = p.group * p.q_len;
 #pragma unroll
-    for (int n = 0; n < RT; ++n) {
+        for (int n = 0; n < RT; ++n) {
+            const int h = 4 * n + (r >> 1);
+            const bool real = h < rows;
+            const T *src = reinterpret_cast<const T *>(p.q) + query_row(p, s, kvh, real ? h : 0) * D + q * (D / 4);
+            float y[D / 4];
 #pragma unroll
-        for (int k = 0; k < 2 * KW; ++k) qb[n][k] = q_s[(n * 2 * KW + k) * 32 + lane];
-        const float2 f = fac_s[4 * n + q];
-        fac[n] = f.x;
-        off_q[n] = f.y;
-    }
-    int lo[RT], hi[RT];  // attended positions
-    int first = 0;       // first position any row attends to
-    if constexpr (kMasked) {
-        if (p.window > 0) first = L - p.q_len - p.window + 1;
+            for (int i = 0; i < KW; ++i) {
+                const uint4 w = real ? *reinterpret_cast<const uint4 *>(src + 8 * i) : make_uint4(0, 0, 0, 0);
+                const float2 a = E::to_float2(w.x), b = E::to_float2(w.y), c = E::to_float2(w.z), d = E::to_float2(w.w);
+                y[8 * i] = a.x, y[8 * i + 1] = a.y, y[8 * i + 2] = b.x, y[8 * i + 3] = b.y;
+                y[8 * i + 4] = c.x, y[8 * i + 5] = c.y, y[8 * i + 6] = d.x, y[8 * i + 7] = d.y;
+            }
+            float mx = 0.f;
 #pragma unroll
-        for (int n = 0; n < RT; ++n) row_range(p, L, 4 * n + q, &lo[n], &hi[n]);
+            for (int i = 0; i < D / 4; i += 2) mx = max3_nan(mx, fabsf(y[i]), fabsf(y[i + 1]));
+            mx = max3_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 1), 0.f);
+            mx = max3_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 2), 0.f);
+            const bool fine = mx <= FLT_MAX;  // no NaN, no infinity
+            int e = 0;
+            if (mx > 0.f && fine) {
+                (void)frexpf(mx, &e);  // mx in [2^(e-1), 2^e)
+                e = min(14 - e, 120);  // mx 2^e in [2^13, 2^14)
+            }
+            const float up = ldexpf(1.f, e);
+            int sum = 0;
+#pragma unroll
+            for (int w = 0; w < KW; ++w)
+#pragma unroll
+                for (int odd = 0; odd < 2; ++odd) {
+                    uint32_t bytes = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int v = fine ? min(__float2int_rn(y[8 * w + 2 * i + odd] * up), 16383) : 0;
+                        sum += v;
+                        bytes |= (uint32_t)(((r & 1) ? v & 127 : v >> 7) & 255) << (8 * i);
+                    }
+                    qb[n][2 * w + odd] = bytes;
+                }
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            const float f = fine ? ldexpf(p.scale_log2, -e) : NAN;
+            fac[n] = __shfl_sync(0xffffffffu, f, 8 * q) * (kOneSum ? 1.f : 0.0625f);
+            off_q[n] = __shfl_sync(0xffffffffu, (float)sum * f, 8 * q);
+            m[n] = -INFINITY;
+            l[n] = z[n] = zw[n] = 0.f;
+            if constexpr (kMasked) row_range(p, L, 4 * n + q, &lo[n], &hi[n]);
+        }
+        if constexpr (kMasked) {
+            lo_any = p.window > 0 ? L - p.q_len - p.window + 1 : 0;
+            lo_all = p.window > 0 ? L - p.window : 0;
+            hi_all = L - p.q_len;
+        }
+        cv = 1.f;
+        limit = 0.f;
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[n][t][i] = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) accw[n][i] = 0.f;
+        }
     }
 
-    // ---- state of rows 4 n + q ----------------------------------------------
-    float m[RT], l[RT], z[RT], zc[RT], acc[NP][MT][4];
-    float cv = 1.f;      // power of two the V scales are multiplied by (warp-uniform)
-    float limit = 0.f;   // kMaxWeightScale / cv once it was chosen
-#pragma unroll
-    for (int n = 0; n < RT; ++n) {
-        m[n] = -INFINITY;
-        l[n] = z[n] = zc[n] = 0.f;
-    }
-#pragma unroll
-    for (int n = 0; n < NP; ++n)
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[n][t][i] = 0.f;
-    const uint32_t ring_addr = smem_addr(ring);
-    const int k_lane = r * (D / 2) + q * (D / 8);
-    const int v_lane = D == 128 ? (lane & 7) * 64 + (lane >> 3) * 16 : ((lane & 7) + 8 * (lane >> 4)) * 32 + ((lane >> 3) & 1) * 16;
-    bool ok = true;
-    int j = 0, st = 0;
-    uint32_t parity = 0;
-#pragma unroll 1
-    for (; j < np; ++j) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&wbar[st], parity))) {
-            ok = false;
-            break;
-        }
-        const unsigned char *stage = ring + st * 4 * kChunk;
+    // Folds the two blocks in `stage` into the state.  tok0: position of the
+    // first token; tokens from tend on are not there.  `release` is called
+    // once the stage is in registers.
+    template <typename F>
+    __device__ __forceinline__ void pair(const unsigned char *stage, int tok0, int tend, int lane, F release) {
+        const int r = lane >> 2, q = lane & 3;
         float2 ke[4], ce[4];  // (scale, low) of the lane's tokens r, 8 + r, 16 + r, 24 + r in K and V
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -320,85 +244,101 @@ __global__ void __launch_bounds__(kWarps * 32, int4_ctas_per_sm(RT)) decode_int4
             ke[i] = int4_ends(*reinterpret_cast<const uint32_t *>(e));
             ce[i] = int4_ends(*reinterpret_cast<const uint32_t *>(e + kChunk));
         }
-        // S^T = U Q^T: even dims' codes, and odd dims' codes times 16
-        float raw[RT][4], x[RT][4];  // T = 16 q . u of the four tokens, the logits minus m
+        // S^T = U Q^T.  kOneSum: all dims' codes 0..15; otherwise the odd dims'
+        // codes stay times 16, in accumulators of their own (one shift less per
+        // word, two multiply-adds more per logit)
+        float raw[RT][4], x[RT][4];  // T of the four tokens, the logits minus m
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             uint32_t k0[KW], k1[KW];
-            load_words<KW>(k0, stage + 2 * b * kChunk + k_lane);
-            load_words<KW>(k1, stage + 2 * b * kChunk + k_lane + 8 * (D / 2));
+            const unsigned char *kp = stage + 2 * b * kChunk + r * (D / 2) + q * (D / 8);
+            load_words<KW>(k0, kp);
+            load_words<KW>(k1, kp + 8 * (D / 2));
+            int ev[RT][4], od[RT][4];
 #pragma unroll
-            for (int n = 0; n < RT; ++n) {
-                int ev[4] = {0, 0, 0, 0}, od[4] = {0, 0, 0, 0};
+            for (int n = 0; n < RT; ++n)
 #pragma unroll
-                for (int w = 0; w < KW; w += 2) {
-                    mma_u8s8(ev, k0[w] & 0x0f0f0f0fu, k1[w] & 0x0f0f0f0fu, k0[w + 1] & 0x0f0f0f0fu,
-                             k1[w + 1] & 0x0f0f0f0fu, qb[n][2 * w], qb[n][2 * w + 2]);
-                    mma_u8s8(od, k0[w] & 0xf0f0f0f0u, k1[w] & 0xf0f0f0f0u, k0[w + 1] & 0xf0f0f0f0u,
-                             k1[w + 1] & 0xf0f0f0f0u, qb[n][2 * w + 1], qb[n][2 * w + 3]);
+                for (int i = 0; i < 4; ++i) ev[n][i] = od[n][i] = 0;
+#pragma unroll
+            for (int w = 0; w < KW; w += 2) {
+                const uint32_t a0 = k0[w] & 0x0f0f0f0fu, a1 = k1[w] & 0x0f0f0f0fu, a2 = k0[w + 1] & 0x0f0f0f0fu,
+                               a3 = k1[w + 1] & 0x0f0f0f0fu;
+#pragma unroll
+                for (int n = 0; n < RT; ++n) mma_u8s8(ev[n], a0, a1, a2, a3, qb[n][2 * w], qb[n][2 * w + 2]);
+                if constexpr (kOneSum) {
+                    const uint32_t c0 = (k0[w] >> 4) & 0x0f0f0f0fu, c1 = (k1[w] >> 4) & 0x0f0f0f0fu,
+                                   c2 = (k0[w + 1] >> 4) & 0x0f0f0f0fu, c3 = (k1[w + 1] >> 4) & 0x0f0f0f0fu;
+#pragma unroll
+                    for (int n = 0; n < RT; ++n) mma_u8s8(ev[n], c0, c1, c2, c3, qb[n][2 * w + 1], qb[n][2 * w + 3]);
+                } else {
+                    const uint32_t c0 = k0[w] & 0xf0f0f0f0u, c1 = k1[w] & 0xf0f0f0f0u, c2 = k0[w + 1] & 0xf0f0f0f0u,
+                                   c3 = k1[w + 1] & 0xf0f0f0f0u;
+#pragma unroll
+                    for (int n = 0; n < RT; ++n) mma_u8s8(od[n], c0, c1, c2, c3, qb[n][2 * w + 1], qb[n][2 * w + 3]);
                 }
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    raw[n][2 * b + i] = (float)((ev[2 * i] * 128 + ev[2 * i + 1]) * 16 + (od[2 * i] * 128 + od[2 * i + 1]));
             }
+#pragma unroll
+            for (int n = 0; n < RT; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int e = ev[n][2 * i] * 128 + ev[n][2 * i + 1];
+                    raw[n][2 * b + i] = (float)(kOneSum ? e : e * 16 + (od[n][2 * i] * 128 + od[n][2 * i + 1]));
+                }
         }
         // V's codes: pairs of tokens, four dims per word
         uint32_t vw[2][D / 32][2];  // [block][group of 32 dims][tokens 2q.., 8 + 2q..]
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-            const uint32_t at = ring_addr + (st * 4 + 2 * b + 1) * kChunk + v_lane;
+            const uint32_t vp = smem_addr(stage) + (2 * b + 1) * kChunk;
             uint32_t w[4];
-            load_matrix4_trans(w, at);
             if constexpr (D == 128) {
                 uint32_t h[4];
+                const uint32_t at = vp + (lane & 7) * 64 + (lane >> 3) * 16;
+                load_matrix4_trans(w, at);
                 load_matrix4_trans(h, at + 8 * 64);
 #pragma unroll
                 for (int g = 0; g < 4; ++g) vw[b][g][0] = w[g], vw[b][g][1] = h[g];
             } else {
+                load_matrix4_trans(w, vp + ((lane & 7) + 8 * (lane >> 4)) * 32 + ((lane >> 3) & 1) * 16);
                 vw[b][0][0] = w[0], vw[b][1][0] = w[1], vw[b][0][1] = w[2], vw[b][1][1] = w[3];
             }
         }
         __syncwarp();
-        if (j + kStages < np) {  // the pair is in registers: its stage may be filled again
-            fence_proxy_async_smem();
-            issue(j + kStages, st);
-        }
-        if (++st == kStages) {
-            st = 0;
-            parity ^= 1;
-        }
+        release();
 
-        const int base = (b0 + 2 * (warp + kWarps * j)) * kBlock + r;  // the lane's first token
-        const bool whole = !kMasked && base - r + 2 * kBlock <= tend;
+        // whole: every row sees all 32 tokens
+        const bool whole = tok0 + 2 * kBlock <= tend && (!kMasked || (tok0 >= lo_all && tok0 + 2 * kBlock - 1 <= hi_all));
         bool dead[RT][4];
         if (!whole) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int tok = base + 8 * i;
+                const int tok = tok0 + 8 * i + r;
                 // rows that no query sees may hold anything
-                if (tok >= tend || (kMasked && tok < first)) ce[i] = make_float2(0.f, 0.f);
+                if (tok >= tend || (kMasked && tok < lo_any)) ce[i] = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int n = 0; n < RT; ++n) dead[n][i] = tok >= tend || (kMasked && (tok < lo[n] || tok > hi[n]));
             }
         }
         auto logits = [&](int n) {  // +inf before the first maximum
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[n][i] = fmaf(ke[i].x * fac[n], raw[n][i], fmaf(ke[i].y, off_q[n], -m[n]));
-                if (!whole && dead[n][i]) x[n][i] = -INFINITY;
+            for (int i = 0; i < 4; ++i) x[n][i] = fmaf(ke[i].x * fac[n], raw[n][i], fmaf(ke[i].y, off_q[n], -m[n]));
+            if (!whole) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (dead[n][i]) x[n][i] = -INFINITY;
             }
         };
         // running maxima, raised only when a logit beats one by 2^8 or a V
         // scale its power of two (NaN takes this way too)
-        const float big4 = fmaxf(fmaxf(fabsf(ce[0].x), fabsf(ce[1].x)), fmaxf(fabsf(ce[2].x), fabsf(ce[3].x)));
-        bool exceed = big4 > limit;
+        float most = -INFINITY;
 #pragma unroll
         for (int n = 0; n < RT; ++n) {
             logits(n);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) exceed = exceed || !(x[n][i] <= kLazyMax);
+            most = max3_nan(most, x[n][0], x[n][1]);
+            most = max3_nan(most, x[n][2], x[n][3]);
         }
-        if (__any_sync(0xffffffffu, exceed)) {
+        const float big4 = fmaxf(fmaxf(fabsf(ce[0].x), fabsf(ce[1].x)), fmaxf(fabsf(ce[2].x), fabsf(ce[3].x)));
+        if (__any_sync(0xffffffffu, big4 > limit || !(most <= kLazyMax))) {
             float big = big4;
 #pragma unroll
             for (int o = 16; o > 2; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
@@ -430,16 +370,19 @@ __global__ void __launch_bounds__(kWarps * 32, int4_ctas_per_sm(RT)) decode_int4
                 l[n] *= alpha;
                 z[n] *= alpha;
                 alpha *= turn;
-                zc[n] *= alpha;
+                zw[n] *= alpha;
+                if constexpr (kSplit) {
 #pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    if constexpr (kSplit) {
+                    for (int t = 0; t < MT; ++t)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) acc[0][t][i] *= alpha;
-                    } else {
+                } else {
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) {
                         acc[n / 2][t][n & 1] *= alpha;
                         acc[n / 2][t][2 + (n & 1)] *= alpha;
                     }
+                    accw[n / 2][n & 1] *= alpha;
                 }
                 logits(n);
             }
@@ -455,88 +398,208 @@ __global__ void __launch_bounds__(kWarps * 32, int4_ctas_per_sm(RT)) decode_int4
                 const float pr = ex2(x[n][i]);
                 l[n] += pr;
                 w[n] = pr * sv;
-                float zz = pr * ce[i].y;
-                if (kMasked && dead[n][i]) w[n] = zz = 0.f;  // a row that does not see a NaN stays clear of it
-                z[n] += zz;
+                float zz = ce[i].y;
+                if (kMasked && !whole && dead[n][i]) w[n] = zz = 0.f;  // a row that does not see a NaN stays clear of it
+                z[n] = fmaf(pr, zz, z[n]);
+                if constexpr (!kSplit) zw[n] += w[n];
             }
-            if constexpr (kSplit) {
-                const __half2 h = __floats2half2_rn(w[0], w[0] - __half2float(__float2half_rn(w[0])));
-                wb[0][i] = transpose8x8(*reinterpret_cast<const uint32_t *>(&h));
-            } else {
 #pragma unroll
-                for (int n = 0; n < NP; ++n) {
-                    const __half2 h = __floats2half2_rn(w[2 * n], w[2 * n + 1]);
-                    const float2 back = __half22float2(h);
-                    zc[2 * n] += w[2 * n] - back.x;
-                    zc[2 * n + 1] += w[2 * n + 1] - back.y;
-                    wb[n][i] = transpose8x8(*reinterpret_cast<const uint32_t *>(&h));
-                }
+            for (int n = 0; n < NP; ++n) {
+                const __half2 h = kSplit ? __floats2half2_rn(w[0], w[0] - __half2float(__float2half_rn(w[0])))
+                                         : __floats2half2_rn(w[(2 * n) % RT], w[(2 * n + 1) % RT]);
+                wb[n][i] = transpose8x8(*reinterpret_cast<const uint32_t *>(&h));
             }
         }
         // O^T += U'^T W^T: tile 2 g + u holds dims 32 g + 4 r + 2 u (and + 1, times 16)
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < 2; ++b) {
 #pragma unroll
             for (int g = 0; g < D / 32; ++g) {
                 const uint32_t a = vw[b][g][0], c = vw[b][g][1], a8 = a >> 8, c8 = c >> 8;
+                const uint32_t a0 = a & 0x000f000fu, a1 = a & 0x00f000f0u, a2 = c & 0x000f000fu, a3 = c & 0x00f000f0u;
+                const uint32_t c0 = a8 & 0x000f000fu, c1 = a8 & 0x00f000f0u, c2 = c8 & 0x000f000fu, c3 = c8 & 0x00f000f0u;
 #pragma unroll
                 for (int n = 0; n < NP; ++n) {
-                    mma_f16(acc[n][2 * g], a & 0x000f000fu, a & 0x00f000f0u, c & 0x000f000fu, c & 0x00f000f0u,
-                            wb[n][2 * b], wb[n][2 * b + 1]);
-                    mma_f16(acc[n][2 * g + 1], a8 & 0x000f000fu, a8 & 0x00f000f0u, c8 & 0x000f000fu, c8 & 0x00f000f0u,
-                            wb[n][2 * b], wb[n][2 * b + 1]);
+                    mma_f16(acc[n][2 * g], a0, a1, a2, a3, wb[n][2 * b], wb[n][2 * b + 1]);
+                    mma_f16(acc[n][2 * g + 1], c0, c1, c2, c3, wb[n][2 * b], wb[n][2 * b + 1]);
                 }
             }
-    }
-    if (!ok) {
-        // A copy never completed (the error word is set): every copy still out
-        // gets one more bounded chance to land before the CTA exits.
-        if (lane == 0)
-            for (int jj = j; jj < j + kStages && jj < np; ++jj)
-                mbar_wait(&wbar[jj % kStages], (jj / kStages) & 1, 200000000ll);
-        atomicOr(&fail_s, 1);
+            if constexpr (!kSplit) {
+                constexpr uint32_t kOnes = 0x3c003c00u;
+#pragma unroll
+                for (int n = 0; n < NP; ++n) mma_f16(accw[n], kOnes, kOnes, kOnes, kOnes, wb[n][2 * b], wb[n][2 * b + 1]);
+            }
+        }
     }
 
-    // ---- merge the warps' states --------------------------------------------
-    __syncthreads();  // every warp is done with its stages; reuse them
-    if (fail_s) return;
+    // The pairs of `span` through the ring.  False when a copy never came (the
+    // error word is set); every copy still out then had one more bounded chance
+    // to land.
+    __device__ __forceinline__ bool run(const DecodeParams &p, Int4Ring<D> &ring, const Int4Span &span, int lane) {
+        const int32_t *row = p.block_tables + (int64_t)span.s * p.max_blocks_per_seq;
+        auto window = [&](int w) -> int32_t {  // the blocks of pairs 16 w .. 16 w + 15, one per lane; -1 past the end
+            const int b = span.first + span.stride * (16 * w + (lane >> 1)) * 2 + (lane & 1);
+            return 16 * w < span.pairs && b < span.end ? (int32_t)checked_block(p, row[b]) : -1;
+        };
+        int32_t cur = window(0), next = window(1);
+        // the loads of pair j (all lanes, j in ascending order): lane i brings
+        // chunk i of the stage (K and V of its first block, K and V of its second)
+        const unsigned char *pool =
+            reinterpret_cast<const unsigned char *>((lane & 1) ? p.v_cache : p.k_cache) + (int64_t)span.kvh * kChunk;
+        const uint32_t block_bytes = (uint32_t)(p.num_kv_heads * kChunk);
+        auto issue = [&](int j, int st) {
+            if ((j & 15) == 0 && j > 0) {
+                cur = next;
+                next = window(j / 16 + 1);
+            }
+            const int32_t phys = __shfl_sync(0xffffffffu, cur, ((j & 15) << 1) + ((lane >> 1) & 1));
+            const bool both = __shfl_sync(0xffffffffu, phys, 2) >= 0;
+            if (lane < 4) {
+                if (lane == 0) mbar_arrive_expect_tx(&ring.bars[st], both ? 4 * kChunk : 2 * kChunk);
+                __syncwarp(15u);
+                if (phys >= 0)
+                    bulk_g2s(ring.base + (st * 4 + lane) * kChunk, pool + (uint64_t)(uint32_t)phys * block_bytes, kChunk,
+                             &ring.bars[st]);
+            }
+        };
+        fence_proxy_async_smem();  // an earlier span's reads of the stages
+        for (int j = 0, st = ring.st; j < kStages && j < span.pairs; ++j) {
+            issue(j, st);
+            if (++st == kStages) st = 0;
+        }
+        start(p, span.s, span.kvh, span.L, lane);
+        const int tend = min(span.L, span.end * kBlock);
+#pragma unroll 1
+        for (int j = 0; j < span.pairs; ++j) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&ring.bars[ring.st], ring.parity))) {
+                for (int k = j; k < j + kStages && k < span.pairs; ++k) {
+                    if (lane == 0) mbar_wait(&ring.bars[ring.st], ring.parity, 200000000ll);
+                    if (++ring.st == kStages) ring.st = 0, ring.parity ^= 1;
+                }
+                return false;
+            }
+            const int st = ring.st;
+            pair(ring.base + st * 4 * kChunk, (span.first + 2 * span.stride * j) * kBlock, tend, lane, [&] {
+                if (j + kStages < span.pairs) {  // the pair is in registers: its stage may be filled again
+                    fence_proxy_async_smem();
+                    issue(j + kStages, st);
+                }
+            });
+            if (++ring.st == kStages) ring.st = 0, ring.parity ^= 1;
+        }
+        return true;
+    }
+
+    // Sums over the warp's lanes; then row 4 n + q has weight l[n], and
+    // output(n, g) its unnormalised dims 32 g + 4 r .. + 3.
+    __device__ __forceinline__ void finish() {
+#pragma unroll
+        for (int n = 0; n < RT; ++n) {
+#pragma unroll
+            for (int o = 16; o > 2; o >>= 1) {
+                l[n] += __shfl_xor_sync(0xffffffffu, l[n], o);
+                z[n] += __shfl_xor_sync(0xffffffffu, z[n], o);
+                if constexpr (!kSplit) zw[n] += __shfl_xor_sync(0xffffffffu, zw[n], o);
+            }
+            if constexpr (!kSplit) z[n] = fmaf(7.5f * (zw[n] - accw[n / 2][n & 1]), 1.f / cv, z[n]);
+        }
+    }
+    __device__ __forceinline__ float4 output(int n, int g) const {
+        const float back = 1.f / cv;  // a power of two
+        float o[4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const float *c = acc[n / 2][2 * g + u];
+            o[2 * u] = fmaf((kSplit ? c[0] + c[1] : c[n & 1]) * kTwo24, back, z[n]);
+            o[2 * u + 1] = fmaf((kSplit ? c[2] + c[3] : c[2 + (n & 1)]) * (kTwo24 / 16.f), back, z[n]);
+        }
+        return make_float4(o[0], o[1], o[2], o[3]);
+    }
+};
+
+// Tiles of 4 query rows a launch for `rows` rows takes: 1, 2 or 4.
+constexpr int int4_row_tiles(int rows) { return rows <= 4 ? 1 : rows <= 8 ? 2 : 4; }
+
+// CTAs per SM: 4 while the state fits 128 registers.
+__host__ __device__ constexpr int int4_ctas_per_sm(int RT) { return RT == 1 ? 4 : RT == 2 ? 3 : 2; }
+
+// Shared memory of a CTA: the warps' rings (reused for the warps' outputs by
+// the partitioned kernel), their m and l, the mbarriers.
+struct Int4Layout {
+    int main, ml_off, bar_off, bytes;
+    __host__ __device__ constexpr Int4Layout(int D, int rows)
+        : main(kWarps * kStages * 4 * int4_chunk_bytes(D) > kWarps * rows * D * 4
+                   ? kWarps * kStages * 4 * int4_chunk_bytes(D)
+                   : kWarps * rows * D * 4),
+          ml_off(main), bar_off(ml_off + 2 * kWarps * rows * 4), bytes(bar_off + kWarps * kStages * 8) {}
+};
+
+template <int D>
+__device__ __forceinline__ Int4Ring<D> make_ring(unsigned char *smem, int bar_off, int warp, int lane) {
+    Int4Ring<D> ring{smem + warp * kStages * 4 * int4_chunk_bytes(D),
+                     reinterpret_cast<uint64_t *>(smem + bar_off) + warp * kStages, 0, 0};
+    if (lane == 0) {
+        for (int i = 0; i < kStages; ++i) mbar_init(&ring.bars[i], 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
+    return ring;
+}
+
+// CTA = (partition, KV head, sequence); warp w takes pairs w, w + 4, ...
+template <typename T, int D, int RT, bool kMasked>
+__global__ void __launch_bounds__(kWarps * 32, int4_ctas_per_sm(RT)) decode_int4_kernel(const DecodeParams p) {
+    using E = Elem<T>;
+    constexpr int RW = 4 * RT;
+    constexpr Int4Layout Lay(D, RW);
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ int fail_s;
+    const int part = blockIdx.x, kvh = blockIdx.y;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, q = lane & 3;
+    pdl_launch_dependents();
+    // Order and lengths are read before the wait for the kernel in front (no
+    // kernel of this library writes them), q and the caches after.
+    const int s = scheduled_seq(p, blockIdx.z, part == 0 && kvh == 0 && tid == 0);
+    const SeqSplit sp = s < 0 ? SeqSplit{0, 0, 0, 0} : seq_split(p, s, part == 0 && kvh == 0 && tid == 0);
+    if (tid == 0) fail_s = 0;
+    Int4Ring<D> ring = make_ring<D>(smem, Lay.bar_off, warp, lane);
+    pdl_wait();
+    if (part >= sp.nparts) return;  // s < 0 too
+    const int rows = p.group * p.q_len;
+    T *out = reinterpret_cast<T *>(p.out);
+    if (sp.L == 0) {
+        for (int i = tid; i < rows * D; i += blockDim.x) out[query_row(p, s, kvh, i / D) * D + i % D] = E::from_float(0.f);
+        return;
+    }
+    const int b0 = sp.bfirst + part * p.part_blocks, b1 = min(b0 + p.part_blocks, sp.nblk);
+    const int pairs = (b1 - b0 + 1) / 2;
+    Int4Warp<T, D, RT, kMasked> w;
+    const Int4Span span{s, kvh, sp.L, b0 + 2 * warp, kWarps, b1, max(0, (pairs - warp + kWarps - 1) / kWarps)};
+    const bool ok = w.run(p, ring, span, lane);
+    __syncthreads();  // fail_s is set to 0, every warp is done with its ring
+    if (!ok) atomicOr(&fail_s, 1);
+    w.finish();
     float *red_acc = reinterpret_cast<float *>(smem);
     float *red_m = reinterpret_cast<float *>(smem + Lay.ml_off), *red_l = red_m + kWarps * RW;
-    const float back = 1.f / cv;  // a power of two
 #pragma unroll
     for (int n = 0; n < RT; ++n) {
         const int h = 4 * n + q;
-#pragma unroll
-        for (int o = 16; o > 2; o >>= 1) {
-            l[n] += __shfl_xor_sync(0xffffffffu, l[n], o);
-            z[n] += __shfl_xor_sync(0xffffffffu, z[n], o);
-            if constexpr (!kSplit) zc[n] += __shfl_xor_sync(0xffffffffu, zc[n], o);
-        }
         if (h >= rows) continue;
-        const float add = kSplit ? z[n] : fmaf(7.5f * zc[n], back, z[n]);
-        float *dst = red_acc + (warp * RW + h) * D + 4 * r;
 #pragma unroll
-        for (int g = 0; g < D / 32; ++g) {
-            float o[4];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const float *c = acc[n / 2][2 * g + u];
-                o[2 * u] = fmaf((kSplit ? c[0] + c[1] : c[n & 1]) * kTwo24, back, add);
-                o[2 * u + 1] = fmaf((kSplit ? c[2] + c[3] : c[2 + (n & 1)]) * (kTwo24 / 16.f), back, add);
-            }
-            *reinterpret_cast<float4 *>(dst + 32 * g) = make_float4(o[0], o[1], o[2], o[3]);
-        }
+        for (int g = 0; g < D / 32; ++g)
+            *reinterpret_cast<float4 *>(red_acc + (warp * RW + h) * D + 32 * g + 4 * r) = w.output(n, g);
         if (r == 0) {
-            red_m[warp * RW + h] = m[n];
-            red_l[warp * RW + h] = l[n];
+            red_m[warp * RW + h] = w.m[n];
+            red_l[warp * RW + h] = w.l[n];
         }
     }
     __syncthreads();
+    if (fail_s) return;
     for (int i = tid; i < rows * D; i += blockDim.x) {
         const int h = i / D, d = i % D;
         float lse;
         const float o = combine_warps<D, RW, kWarps>(red_m, red_l, red_acc, h, d, &lse) * p.v_scale;
-        const int64_t qr = row_of(h);
+        const int64_t qr = query_row(p, s, kvh, h);
         if (sp.nparts == 1) {
             out[qr * D + d] = E::from_float(o);
         } else {
@@ -547,33 +610,271 @@ __global__ void __launch_bounds__(kWarps * 32, int4_ctas_per_sm(RT)) decode_int4
     }
 }
 
+// ---------------------------------------------------------------------------
+// equal shares
+// ---------------------------------------------------------------------------
+// The flat order: sequences, in each its KV heads, in each kStartCost places
+// for what a context costs before its first block (its query rows, the first
+// copies' latency) and then its blocks.  Warp w owns places [w W, (w + 1) W).
+constexpr int kStartCost = 8;
+constexpr int kMinShare = kStartCost + 8;
+
+// Blocks that sequence s's queries attend to, from which entry, and its length.
+struct Int4Seq {
+    int L, first, n;
+};
+__device__ __forceinline__ Int4Seq int4_seq(const DecodeParams &p, int s, bool report) {
+    const SeqSplit sp = seq_split(p, s, report);  // max_parts is 1: longer contexts are flagged and cut
+    return {sp.L, sp.bfirst, min(sp.nblk - sp.bfirst, p.part_blocks)};
+}
+
+__device__ __forceinline__ int64_t int4_share(int64_t total, int64_t warps) {
+    const int64_t w = (total + warps - 1) / warps;
+    return w < kMinShare ? kMinShare : w;
+}
+
 template <typename T, int D, int RT, bool kMasked>
-cudaError_t launch_int4_t(const DecodeParams &p, cudaStream_t stream) {
-    auto kern = decode_int4_kernel<T, D, RT, kMasked>;
-    static FuncAttrCache attrs;
+__global__ void __launch_bounds__(kWarps * 32, int4_ctas_per_sm(RT))
+    decode_int4_balanced_kernel(const DecodeParams p, int64_t *starts) {
+    using E = Elem<T>;
+    constexpr Int4Layout Lay(D, 4 * RT);
+    constexpr int kThreads = kWarps * 32;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ int64_t chunk_end[kThreads];
+    __shared__ int64_t warp_sum[kWarps];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, q = lane & 3;
+    pdl_launch_dependents();
+    Int4Ring<D> ring = make_ring<D>(smem, Lay.bar_off, warp, lane);
+    // places of all sequences: each thread sums a run of them, then a scan
+    // (before the wait for the kernel in front: no kernel of this library
+    // writes lengths)
+    const int per = (p.num_seqs + kThreads - 1) / kThreads, s0 = min(tid * per, p.num_seqs), s1 = min(s0 + per, p.num_seqs);
+    const bool report = blockIdx.x == 0;
+    int64_t sum = 0;
+    for (int s = s0; s < s1; ++s) sum += (int64_t)p.num_kv_heads * (kStartCost + int4_seq(p, s, report).n);
+    int64_t scan = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, scan, o);
+        if (lane >= o) scan += v;
+    }
+    if (lane == 31) warp_sum[warp] = scan;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) scan += warp_sum[w];
+    chunk_end[tid] = scan;
+    __syncthreads();
+    const int64_t total = chunk_end[kThreads - 1];
+    pdl_wait();
+    if (blockIdx.x == 0) {  // for the merge
+        int64_t at = scan - sum;
+        for (int s = s0; s < s1; ++s) {
+            starts[s] = at;
+            at += (int64_t)p.num_kv_heads * (kStartCost + int4_seq(p, s, false).n);
+        }
+        if (tid == 0) starts[p.num_seqs] = total;
+        if (p.seq_order)  // results and shares do not depend on it; it is checked all the same
+            for (int i = tid; i < p.num_seqs; i += kThreads) (void)scheduled_seq(p, i, true);
+    }
+    const int64_t me = (int64_t)blockIdx.x * kWarps + warp;
+    const int64_t share = int4_share(total, (int64_t)gridDim.x * kWarps);
+    int64_t x = me * share;
+    const int64_t xend = min(x + share, total);
+    if (x >= xend) return;
+    // the sequence of place x: the thread whose run holds it, then its run
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) c += __popc(__ballot_sync(0xffffffffu, chunk_end[32 * i + lane] <= x));
+    int s = c * per;
+    int64_t at = c == 0 ? 0 : chunk_end[c - 1];  // first place of sequence s
+    Int4Seq seq = int4_seq(p, s, false);
+    while (x >= at + (int64_t)p.num_kv_heads * (kStartCost + seq.n)) {
+        at += (int64_t)p.num_kv_heads * (kStartCost + seq.n);
+        seq = int4_seq(p, ++s, false);
+    }
+    int kvh = (int)((x - at) / (kStartCost + seq.n));
+    at += (int64_t)kvh * (kStartCost + seq.n);  // first place of (s, kvh)
+    const int rows = p.group * p.q_len;
+    T *out = reinterpret_cast<T *>(p.out);
+    for (;;) {
+        const int64_t blocks_at = at + kStartCost;
+        const int from = (int)max((int64_t)0, x - blocks_at), to = (int)min((int64_t)seq.n, xend - blocks_at);
+        if (seq.n == 0 && x <= at) {  // an empty context: zero rows
+            for (int i = lane; i < rows * D; i += 32) out[query_row(p, s, kvh, i / D) * D + i % D] = E::from_float(0.f);
+        } else if (to > from) {
+            Int4Warp<T, D, RT, kMasked> w;
+            const Int4Span span{s, kvh, seq.L, seq.first + from, 1, seq.first + to, (to - from + 1) / 2};
+            if (!w.run(p, ring, span, lane)) return;
+            w.finish();
+            const bool all = from == 0 && to == seq.n;
+            const int64_t slot = 2 * me + (from == 0 ? 1 : 0);  // the context's first piece, or a later one
+#pragma unroll
+            for (int n = 0; n < RT; ++n) {
+                const int h = 4 * n + q;
+                if (h >= rows) continue;
+                const float inv = w.l[n] == 0.f ? 0.f : p.v_scale / w.l[n];
+                const int64_t qr = query_row(p, s, kvh, h);
+#pragma unroll
+                for (int g = 0; g < D / 32; ++g) {
+                    const float4 v = w.output(n, g);
+                    const float4 o = w.l[n] == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                                   : make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+                    if (all) {
+                        const typename E::T2 a = {E::from_float(o.x), E::from_float(o.y)};
+                        const typename E::T2 b = {E::from_float(o.z), E::from_float(o.w)};
+                        *reinterpret_cast<uint2 *>(out + qr * D + 32 * g + 4 * r) =
+                            make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+                    } else {
+                        *reinterpret_cast<float4 *>(p.ws_o + (slot * rows + h) * D + 32 * g + 4 * r) = o;
+                    }
+                }
+                if (!all && r == 0) {
+                    const float lse = w.l[n] == 0.f ? -INFINITY : w.m[n] + log2f(w.l[n]);
+                    p.ws_lse[slot * rows + h] = lse != lse ? 0.f : lse;  // the NaN is in o: the merge must not skip it
+                }
+            }
+        }
+        at = blocks_at + seq.n;
+        x = at;
+        if (x >= xend) return;
+        if (++kvh == p.num_kv_heads) {
+            kvh = 0;
+            seq = int4_seq(p, ++s, false);
+        }
+    }
+}
+
+// Joins the pieces of contexts that no warp held whole: out = sum_i 2^(lse_i -
+// M) o_i / sum_i 2^(lse_i - M), M = max lse.  CTA = (4 / kRowWarps query rows
+// of a sequence): kRowWarps warps share a row's pieces (1 where contexts have
+// few, 4 where they have many).
+template <typename T, int D, int kRowWarps>
+__global__ void __launch_bounds__(128) merge_int4_kernel(const DecodeParams p, const int64_t *starts, int64_t warps) {
+    using E = Elem<T>;
+    constexpr int kV = D / 32;
+    __shared__ float red[4][D + 1];
+    const int s = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_launch_dependents();
+    const Int4Seq seq = int4_seq(p, s, false);
+    const int rows = p.group * p.q_len;
+    const int row = blockIdx.x * (4 / kRowWarps) + warp / kRowWarps;  // query row of the sequence, KV head by KV head
+    const bool real = row < p.num_kv_heads * rows;
+    const int kvh = real ? row / rows : 0, h = real ? row % rows : 0;
+    pdl_wait();
+    const int64_t share = int4_share(starts[p.num_seqs], warps);
+    const int64_t at = starts[s] + (int64_t)kvh * (kStartCost + seq.n) + kStartCost;
+    const int64_t wa = at / share, wb = (at + seq.n - 1) / share;
+    const int pieces = seq.n == 0 || !real ? 0 : (int)(wb - wa + 1);
+    if (kRowWarps == 4 ? pieces <= 1 : __all_sync(0xffffffffu, pieces <= 1)) return;  // written by its warp
+    auto slot = [&](int i) -> int64_t { return (i == 0 ? 2 * wa + 1 : 2 * (wa + i)) * rows + h; };
+    float M = -INFINITY;
+    for (int i = lane; i < pieces; i += 32) M = fmaxf(M, p.ws_lse[slot(i)]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float acc[kV] = {}, wsum = 0.f;
+    if (M != -INFINITY) {
+        constexpr int kInFlight = 4;
+        for (int i0 = warp % kRowWarps; i0 < pieces; i0 += kRowWarps * kInFlight) {
+            float w[kInFlight], v[kInFlight][kV];
+#pragma unroll
+            for (int k = 0; k < kInFlight; ++k) {
+                const int i = i0 + k * kRowWarps;
+                const float lse = i < pieces ? p.ws_lse[slot(i)] : -INFINITY;
+                w[k] = 0.f;
+#pragma unroll
+                for (int e = 0; e < kV; ++e) v[k][e] = 0.f;
+                if (lse != -INFINITY) {
+                    w[k] = exp2f(lse - M);
+                    const float *src = p.ws_o + slot(i) * D + lane * kV;
+#pragma unroll
+                    for (int e = 0; e < kV; e += 2) {
+                        const float2 f = *reinterpret_cast<const float2 *>(src + e);
+                        v[k][e] = f.x;
+                        v[k][e + 1] = f.y;
+                    }
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kInFlight; ++k) {
+                wsum += w[k];
+#pragma unroll
+                for (int e = 0; e < kV; ++e) acc[e] = fmaf(w[k], v[k][e], acc[e]);
+            }
+        }
+    }
+    if constexpr (kRowWarps == 4) {
+#pragma unroll
+        for (int e = 0; e < kV; ++e) red[warp][lane * kV + e] = acc[e];
+        if (lane == 0) red[warp][D] = wsum;
+        __syncthreads();
+        if (warp != 0) return;
+        wsum = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) wsum += red[k][D];
+#pragma unroll
+        for (int e = 0; e < kV; ++e) {
+            acc[e] = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[e] += red[k][lane * kV + e];
+        }
+    }
+    if (pieces <= 1) return;
+    const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
+    T *dst = reinterpret_cast<T *>(p.out) + query_row(p, s, kvh, h) * D + lane * kV;
+#pragma unroll
+    for (int e = 0; e < kV; e += 2) {
+        const typename E::T2 a = {E::from_float(acc[e] * inv), E::from_float(acc[e + 1] * inv)};
+        *reinterpret_cast<typename E::T2 *>(dst + e) = a;
+    }
+}
+
+template <typename T, int D, int RT, bool kMasked>
+cudaError_t launch_int4_t(const DecodeParams &p, int64_t *starts, int ctas, cudaStream_t stream) {
     constexpr int kSmem = Int4Layout(D, 4 * RT).bytes;
+    if (!starts) {
+        auto kern = decode_int4_kernel<T, D, RT, kMasked>;
+        static FuncAttrCache attrs;
+        cudaError_t e = ensure_smem(kern, kSmem, attrs, /*max_carveout=*/true);
+        if (e != cudaSuccess) return e;
+        e = launch_pdl(kern, dim3(p.max_parts, p.num_kv_heads, p.num_seqs), dim3(kWarps * 32), kSmem, stream, p);
+        if (e != cudaSuccess || p.max_parts == 1) return e;
+        return launch_merge_partitions(p, std::is_same<T, __nv_bfloat16>::value ? PA_BF16 : PA_F16, D, stream);
+    }
+    auto kern = decode_int4_balanced_kernel<T, D, RT, kMasked>;
+    static FuncAttrCache attrs;
     cudaError_t e = ensure_smem(kern, kSmem, attrs, /*max_carveout=*/true);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(kern, dim3(p.max_parts, p.num_kv_heads, p.num_seqs), dim3(kWarps * 32), kSmem, stream, p);
-    if (e != cudaSuccess || p.max_parts == 1) return e;
-    return launch_merge_partitions(p, std::is_same<T, __nv_bfloat16>::value ? PA_BF16 : PA_F16, D, stream);
+    e = launch_pdl(kern, dim3(ctas), dim3(kWarps * 32), kSmem, stream, p, starts);
+    if (e != cudaSuccess) return e;
+    // pieces a context may have: many on few sequences
+    const int64_t warps = (int64_t)ctas * kWarps;
+    const int rows = p.num_heads * p.q_len;
+    const bool many = warps > 8 * (int64_t)p.num_seqs * p.num_kv_heads;
+    const dim3 grid(many ? rows : (rows + 3) / 4, p.num_seqs);
+    return many ? launch_pdl(merge_int4_kernel<T, D, 4>, grid, dim3(128), 0, stream, p, (const int64_t *)starts, warps)
+                : launch_pdl(merge_int4_kernel<T, D, 1>, grid, dim3(128), 0, stream, p, (const int64_t *)starts, warps);
 }
 
 template <typename T, int D>
-cudaError_t launch_int4_d(const DecodeParams &p, int rows, cudaStream_t stream) {
+cudaError_t launch_int4_d(const DecodeParams &p, int rows, int64_t *starts, int ctas, cudaStream_t stream) {
     const bool masked = decode_masked(p);
-    if (rows <= 4) return masked ? launch_int4_t<T, D, 1, true>(p, stream) : launch_int4_t<T, D, 1, false>(p, stream);
-    if (rows <= 8) return masked ? launch_int4_t<T, D, 2, true>(p, stream) : launch_int4_t<T, D, 2, false>(p, stream);
-    return masked ? launch_int4_t<T, D, 4, true>(p, stream) : launch_int4_t<T, D, 4, false>(p, stream);
+    switch (int4_row_tiles(rows)) {
+        case 1: return masked ? launch_int4_t<T, D, 1, true>(p, starts, ctas, stream) : launch_int4_t<T, D, 1, false>(p, starts, ctas, stream);
+        case 2: return masked ? launch_int4_t<T, D, 2, true>(p, starts, ctas, stream) : launch_int4_t<T, D, 2, false>(p, starts, ctas, stream);
+        default: return masked ? launch_int4_t<T, D, 4, true>(p, starts, ctas, stream) : launch_int4_t<T, D, 4, false>(p, starts, ctas, stream);
+    }
 }
 
 }  // namespace
 
-cudaError_t launch_decode_int4(const DecodeParams &p, int dtype, int head_dim, int rows, cudaStream_t stream) {
+int decode_int4_ctas(int rows, int sms) { return sms * int4_ctas_per_sm(int4_row_tiles(rows)); }
+
+cudaError_t launch_decode_int4(const DecodeParams &p, int dtype, int head_dim, int rows, int64_t *starts, int ctas,
+                               cudaStream_t stream) {
     if (dtype == PA_F16)
-        return head_dim == 64 ? launch_int4_d<__half, 64>(p, rows, stream) : launch_int4_d<__half, 128>(p, rows, stream);
-    return head_dim == 64 ? launch_int4_d<__nv_bfloat16, 64>(p, rows, stream)
-                          : launch_int4_d<__nv_bfloat16, 128>(p, rows, stream);
+        return head_dim == 64 ? launch_int4_d<__half, 64>(p, rows, starts, ctas, stream)
+                              : launch_int4_d<__half, 128>(p, rows, starts, ctas, stream);
+    return head_dim == 64 ? launch_int4_d<__nv_bfloat16, 64>(p, rows, starts, ctas, stream)
+                          : launch_int4_d<__nv_bfloat16, 128>(p, rows, starts, ctas, stream);
 }
 
 }  // namespace pa
