@@ -83,6 +83,14 @@ __device__ __forceinline__ void mma_u8s8(int (&d)[4], uint32_t a0, uint32_t a1, 
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// D = A B: the first of a chain.
+__device__ __forceinline__ void mma_u8s8_first(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(0));
+}
+
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t r;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
@@ -91,16 +99,18 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 
 // N 32-bit words from shared memory (N = 1, 2 or 4, aligned to N words).
 template <int N>
-__device__ __forceinline__ void load_words(uint32_t (&w)[N], const unsigned char *p) {
-    if constexpr (N == 4) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(p);
-        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-    } else if constexpr (N == 2) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(p);
-        w[0] = v.x, w[1] = v.y;
-    } else {
-        w[0] = *reinterpret_cast<const uint32_t *>(p);
-    }
+__device__ __forceinline__ void load_words(uint32_t (&w)[N], uint32_t addr) {
+    if constexpr (N == 4)
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr) : "memory");
+    else if constexpr (N == 2)
+        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
+    else
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ float2 load_ends(uint32_t addr) {
+    uint32_t w[1];
+    load_words<1>(w, addr);
+    return int4_ends(w[0]);
 }
 
 // Four 8x8 matrices of 16-bit elements, each transposed: lane (r, q) gets
@@ -231,18 +241,19 @@ struct Int4Warp {
         }
     }
 
-    // Folds the two blocks in `stage` into the state.  tok0: position of the
-    // first token; tokens from tend on are not there.  `release` is called
-    // once the stage is in registers.
-    template <typename F>
-    __device__ __forceinline__ void pair(const unsigned char *stage, int tok0, int tend, int lane, F release) {
+    // Folds the two blocks at shared address `stage` into the state.  kEdge: not
+    // every row sees all 32 tokens; tok0 is the position of the first, tokens
+    // from tend on are not there.  `release` is called once the stage is in
+    // registers.
+    template <bool kEdge, typename F>
+    __device__ __forceinline__ void pair(uint32_t stage, int tok0, int tend, int lane, F release) {
         const int r = lane >> 2, q = lane & 3;
         float2 ke[4], ce[4];  // (scale, low) of the lane's tokens r, 8 + r, 16 + r, 24 + r in K and V
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const unsigned char *e = stage + 2 * (i >> 1) * kChunk + int4_ends_offset(D) + 4 * (8 * (i & 1) + r);
-            ke[i] = int4_ends(*reinterpret_cast<const uint32_t *>(e));
-            ce[i] = int4_ends(*reinterpret_cast<const uint32_t *>(e + kChunk));
+            const uint32_t e = stage + 4 * r + 2 * (i >> 1) * kChunk + int4_ends_offset(D) + 32 * (i & 1);
+            ke[i] = load_ends(e);
+            ce[i] = load_ends(e + kChunk);
         }
         // S^T = U Q^T.  kOneSum: all dims' codes 0..15; otherwise the odd dims'
         // codes stay times 16, in accumulators of their own (one shift less per
@@ -251,20 +262,19 @@ struct Int4Warp {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             uint32_t k0[KW], k1[KW];
-            const unsigned char *kp = stage + 2 * b * kChunk + r * (D / 2) + q * (D / 8);
+            const uint32_t kp = stage + r * (D / 2) + q * (D / 8) + 2 * b * kChunk;
             load_words<KW>(k0, kp);
             load_words<KW>(k1, kp + 8 * (D / 2));
             int ev[RT][4], od[RT][4];
-#pragma unroll
-            for (int n = 0; n < RT; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) ev[n][i] = od[n][i] = 0;
 #pragma unroll
             for (int w = 0; w < KW; w += 2) {
                 const uint32_t a0 = k0[w] & 0x0f0f0f0fu, a1 = k1[w] & 0x0f0f0f0fu, a2 = k0[w + 1] & 0x0f0f0f0fu,
                                a3 = k1[w + 1] & 0x0f0f0f0fu;
 #pragma unroll
-                for (int n = 0; n < RT; ++n) mma_u8s8(ev[n], a0, a1, a2, a3, qb[n][2 * w], qb[n][2 * w + 2]);
+                for (int n = 0; n < RT; ++n) {
+                    if (w == 0) mma_u8s8_first(ev[n], a0, a1, a2, a3, qb[n][2 * w], qb[n][2 * w + 2]);
+                    else mma_u8s8(ev[n], a0, a1, a2, a3, qb[n][2 * w], qb[n][2 * w + 2]);
+                }
                 if constexpr (kOneSum) {
                     const uint32_t c0 = (k0[w] >> 4) & 0x0f0f0f0fu, c1 = (k1[w] >> 4) & 0x0f0f0f0fu,
                                    c2 = (k0[w + 1] >> 4) & 0x0f0f0f0fu, c3 = (k1[w + 1] >> 4) & 0x0f0f0f0fu;
@@ -274,7 +284,10 @@ struct Int4Warp {
                     const uint32_t c0 = k0[w] & 0xf0f0f0f0u, c1 = k1[w] & 0xf0f0f0f0u, c2 = k0[w + 1] & 0xf0f0f0f0u,
                                    c3 = k1[w + 1] & 0xf0f0f0f0u;
 #pragma unroll
-                    for (int n = 0; n < RT; ++n) mma_u8s8(od[n], c0, c1, c2, c3, qb[n][2 * w + 1], qb[n][2 * w + 3]);
+                    for (int n = 0; n < RT; ++n) {
+                        if (w == 0) mma_u8s8_first(od[n], c0, c1, c2, c3, qb[n][2 * w + 1], qb[n][2 * w + 3]);
+                        else mma_u8s8(od[n], c0, c1, c2, c3, qb[n][2 * w + 1], qb[n][2 * w + 3]);
+                    }
                 }
             }
 #pragma unroll
@@ -289,7 +302,7 @@ struct Int4Warp {
         uint32_t vw[2][D / 32][2];  // [block][group of 32 dims][tokens 2q.., 8 + 2q..]
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-            const uint32_t vp = smem_addr(stage) + (2 * b + 1) * kChunk;
+            const uint32_t vp = stage + (2 * b + 1) * kChunk;
             uint32_t w[4];
             if constexpr (D == 128) {
                 uint32_t h[4];
@@ -306,10 +319,8 @@ struct Int4Warp {
         __syncwarp();
         release();
 
-        // whole: every row sees all 32 tokens
-        const bool whole = tok0 + 2 * kBlock <= tend && (!kMasked || (tok0 >= lo_all && tok0 + 2 * kBlock - 1 <= hi_all));
         bool dead[RT][4];
-        if (!whole) {
+        if constexpr (kEdge) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int tok = tok0 + 8 * i + r;
@@ -322,7 +333,7 @@ struct Int4Warp {
         auto logits = [&](int n) {  // +inf before the first maximum
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[n][i] = fmaf(ke[i].x * fac[n], raw[n][i], fmaf(ke[i].y, off_q[n], -m[n]));
-            if (!whole) {
+            if constexpr (kEdge) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (dead[n][i]) x[n][i] = -INFINITY;
@@ -357,7 +368,7 @@ struct Int4Warp {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     float v = fmaf(ke[i].x * fac[n], raw[n][i], ke[i].y * off_q[n]);
-                    if (!whole && dead[n][i]) v = -INFINITY;
+                    if (kEdge && dead[n][i]) v = -INFINITY;
                     bm = fmaxf(bm, v != v ? 0.f : v);  // a NaN row gets a finite maximum and NaN sums
                 }
 #pragma unroll
@@ -399,7 +410,7 @@ struct Int4Warp {
                 l[n] += pr;
                 w[n] = pr * sv;
                 float zz = ce[i].y;
-                if (kMasked && !whole && dead[n][i]) w[n] = zz = 0.f;  // a row that does not see a NaN stays clear of it
+                if (kEdge && kMasked && dead[n][i]) w[n] = zz = 0.f;  // a row that does not see a NaN stays clear of it
                 z[n] = fmaf(pr, zz, z[n]);
                 if constexpr (!kSplit) zw[n] += w[n];
             }
@@ -456,7 +467,6 @@ struct Int4Warp {
             const bool both = __shfl_sync(0xffffffffu, phys, 2) >= 0;
             if (lane < 4) {
                 if (lane == 0) mbar_arrive_expect_tx(&ring.bars[st], both ? 4 * kChunk : 2 * kChunk);
-                __syncwarp(15u);
                 if (phys >= 0)
                     bulk_g2s(ring.base + (st * 4 + lane) * kChunk, pool + (uint64_t)(uint32_t)phys * block_bytes, kChunk,
                              &ring.bars[st]);
@@ -469,6 +479,7 @@ struct Int4Warp {
         }
         start(p, span.s, span.kvh, span.L, lane);
         const int tend = min(span.L, span.end * kBlock);
+        const uint32_t ring_addr = smem_addr(ring.base);
 #pragma unroll 1
         for (int j = 0; j < span.pairs; ++j) {
             if (!__all_sync(0xffffffffu, mbar_wait(&ring.bars[ring.st], ring.parity))) {
@@ -478,13 +489,17 @@ struct Int4Warp {
                 }
                 return false;
             }
-            const int st = ring.st;
-            pair(ring.base + st * 4 * kChunk, (span.first + 2 * span.stride * j) * kBlock, tend, lane, [&] {
+            const int st = ring.st, tok0 = (span.first + 2 * span.stride * j) * kBlock;
+            const uint32_t stage = ring_addr + st * 4 * kChunk;
+            auto release = [&] {
                 if (j + kStages < span.pairs) {  // the pair is in registers: its stage may be filled again
                     fence_proxy_async_smem();
                     issue(j + kStages, st);
                 }
-            });
+            };
+            const bool whole = tok0 + 2 * kBlock <= tend && (!kMasked || (tok0 >= lo_all && tok0 + 2 * kBlock - 1 <= hi_all));
+            if (whole) pair<false>(stage, tok0, tend, lane, release);
+            else pair<true>(stage, tok0, tend, lane, release);
             if (++ring.st == kStages) ring.st = 0, ring.parity ^= 1;
         }
         return true;
