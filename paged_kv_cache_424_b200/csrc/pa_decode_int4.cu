@@ -47,8 +47,8 @@
 // head, sequence), the warps take every 4th pair of blocks and merge their
 // states in shared memory; used for partitions that the caller sized and for
 // short contexts.  decode_int4_balanced_kernel: one wave of resident warps,
-// each taking an equal share of all (sequence, KV head, block) in their flat
-// order, whatever the lengths; a piece of a context that its warp does not
+// in teams on neighbouring KV heads, each team taking an equal share of all
+// blocks in their flat order, whatever the lengths; a piece of a context that its warp does not
 // hold whole goes to the workspace, and merge_int4_kernel joins the pieces.
 #include <cfloat>
 #include <type_traits>
@@ -305,27 +305,6 @@ struct Int4Warp {
                     raw[n][2 * b + i] = (float)(kOneSum ? e : e * 16 + (od[n][2 * i] * 128 + od[n][2 * i + 1]));
                 }
         }
-        // V's codes: pairs of tokens, four dims per word
-        uint32_t vw[2][D / 32][2];  // [block][group of 32 dims][tokens 2q.., 8 + 2q..]
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const uint32_t vp = stage + (2 * b + 1) * kChunk;
-            uint32_t w[4];
-            if constexpr (D == 128) {
-                uint32_t h[4];
-                const uint32_t at = vp + (lane & 7) * 64 + (lane >> 3) * 16;
-                load_matrix4_trans(w, at);
-                load_matrix4_trans(h, at + 8 * 64);
-#pragma unroll
-                for (int g = 0; g < 4; ++g) vw[b][g][0] = w[g], vw[b][g][1] = h[g];
-            } else {
-                load_matrix4_trans(w, vp + ((lane & 7) + 8 * (lane >> 4)) * 32 + ((lane >> 3) & 1) * 16);
-                vw[b][0][0] = w[0], vw[b][1][0] = w[1], vw[b][0][1] = w[2], vw[b][1][1] = w[3];
-            }
-        }
-        __syncwarp();
-        release();
-
         bool dead[RT][4];
         if constexpr (kEdge) {
 #pragma unroll
@@ -405,6 +384,27 @@ struct Int4Warp {
                 logits(n);
             }
         }
+        // V's codes: pairs of tokens, four dims per word
+        uint32_t vw[2][D / 32][2];  // [block][group of 32 dims][tokens 2q.., 8 + 2q..]
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const uint32_t vp = stage + (2 * b + 1) * kChunk;
+            uint32_t w[4];
+            if constexpr (D == 128) {
+                uint32_t h[4];
+                const uint32_t at = vp + (lane & 7) * 64 + (lane >> 3) * 16;
+                load_matrix4_trans(w, at);
+                load_matrix4_trans(h, at + 8 * 64);
+#pragma unroll
+                for (int g = 0; g < 4; ++g) vw[b][g][0] = w[g], vw[b][g][1] = h[g];
+            } else {
+                load_matrix4_trans(w, vp + ((lane & 7) + 8 * (lane >> 4)) * 32 + ((lane >> 3) & 1) * 16);
+                vw[b][0][0] = w[0], vw[b][1][0] = w[1], vw[b][0][1] = w[2], vw[b][1][1] = w[3];
+            }
+        }
+        __syncwarp();
+        release();
+
         // weights, turned into the second product's operand
         uint32_t wb[NP][4];
 #pragma unroll
@@ -461,32 +461,26 @@ struct Int4Warp {
             return 16 * w < span.pairs ? (int32_t)checked_block(p, row[min(b, span.end - 1)]) : 0;
         };
         int32_t cur = window(0), next = window(1);
+        // lanes 0 .. 15 bring K's chunk of a block, lanes 16 .. 31 V's, 256 bytes
+        // of each at a time: two addresses per pair, and a chunk's bytes together
         const uint32_t block_bytes = (uint32_t)(p.num_kv_heads * kChunk);
-        const int64_t head = (int64_t)span.kvh * kChunk;
-        const unsigned char *kp = reinterpret_cast<const unsigned char *>(p.k_cache) + head + 16 * lane;
-        const unsigned char *vp = reinterpret_cast<const unsigned char *>(p.v_cache) + head + 16 * lane;
-        // the chunks' last 64 bytes: lanes 0 .. 15, four per chunk
-        const int tail_chunk = lane >> 2;
-        const unsigned char *tp = reinterpret_cast<const unsigned char *>((tail_chunk & 1) ? p.v_cache : p.k_cache) + head +
-                                  8 * D + 16 * (lane & 3);
-        const uint32_t ring_lane = ring + 16 * lane, ring_tail = ring + tail_chunk * kChunk + 8 * D + 16 * (lane & 3);
+        const unsigned char *pool = reinterpret_cast<const unsigned char *>((lane & 16) ? p.v_cache : p.k_cache) +
+                                    (int64_t)span.kvh * kChunk + 16 * (lane & 15);
+        const uint32_t ring_lane = ring + (lane >> 4) * kChunk + 16 * (lane & 15);
         auto issue = [&](int j, int st) {  // pair j (ascending) into stage st
             if ((j & 15) == 0 && j > 0) {
                 cur = next;
                 next = window(j / 16 + 1);
             }
-            const uint32_t b0 = (uint32_t)__shfl_sync(0xffffffffu, cur, (j & 15) << 1);
-            const uint32_t b1 = (uint32_t)__shfl_sync(0xffffffffu, cur, ((j & 15) << 1) + 1);
-            const uint64_t o0 = (uint64_t)b0 * block_bytes, o1 = (uint64_t)b1 * block_bytes;
-            const uint32_t dst = ring_lane + st * 4 * kChunk;
 #pragma unroll
-            for (int i = 0; i < 8 * D; i += 512) {
-                copy16(dst + i, kp + o0 + i);
-                copy16(dst + kChunk + i, vp + o0 + i);
-                copy16(dst + 2 * kChunk + i, kp + o1 + i);
-                copy16(dst + 3 * kChunk + i, vp + o1 + i);
+            for (int b = 0; b < 2; ++b) {
+                const uint32_t block = (uint32_t)__shfl_sync(0xffffffffu, cur, ((j & 15) << 1) + b);
+                const unsigned char *src = pool + (uint64_t)block * block_bytes;
+                const uint32_t dst = ring_lane + (st * 4 + 2 * b) * kChunk;
+#pragma unroll
+                for (int i = 0; i < 8 * D; i += 256) copy16(dst + i, src + i);
+                if ((lane & 15) < 4) copy16(dst + 8 * D, src + 8 * D);
             }
-            if (lane < 16) copy16(ring_tail + st * 4 * kChunk, tp + (lane < 8 ? o0 : o1));
         };
 #pragma unroll
         for (int j = 0; j < kStages; ++j) {
@@ -620,9 +614,14 @@ __global__ void __launch_bounds__(kWarps * 32, int4_ctas_per_sm(RT)) decode_int4
 // ---------------------------------------------------------------------------
 // equal shares
 // ---------------------------------------------------------------------------
-// The flat order: sequences, in each its KV heads, in each kStartCost places
-// for what a context costs before its first block (its query rows, the first
-// copies' latency) and then its blocks.  Warp w owns places [w W, (w + 1) W).
+// A team of 2^team_bits warps (4, 2 or 1, whatever divides num_kv_heads) takes
+// as many neighbouring KV heads of the same blocks, a warp each: the team's
+// chunks of a block are one run of DRAM (measured, reads alone: 6.4 TB/s against
+// 5.9-6.2 with every warp on a context of its own; the 4-token 8B step 210 ->
+// 168 us).  The flat order: sequences, in each its head groups, in each
+// kStartCost places for what a context costs before its first block (its query
+// rows, the first copies' latency) and then its blocks.  Team t owns places
+// [t W, (t + 1) W).
 constexpr int kStartCost = 8;
 constexpr int kMinShare = kStartCost + 8;
 
@@ -642,7 +641,7 @@ __device__ __forceinline__ int64_t int4_share(int64_t total, int64_t warps) {
 
 template <typename T, int D, int RT, bool kMasked>
 __global__ void __launch_bounds__(kWarps * 32, int4_ctas_per_sm(RT))
-    decode_int4_balanced_kernel(const DecodeParams p, int64_t *starts) {
+    decode_int4_balanced_kernel(const DecodeParams p, int64_t *starts, const int team_bits) {
     using E = Elem<T>;
     constexpr int kThreads = kWarps * 32;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -651,13 +650,14 @@ __global__ void __launch_bounds__(kWarps * 32, int4_ctas_per_sm(RT))
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, q = lane & 3;
     pdl_launch_dependents();
     const uint32_t ring = smem_addr(smem) + warp * kStages * 4 * int4_chunk_bytes(D);
+    const int groups = p.num_kv_heads >> team_bits, member = warp & ((1 << team_bits) - 1);
     // places of all sequences: each thread sums a run of them, then a scan
     // (before the wait for the kernel in front: no kernel of this library
     // writes lengths)
     const int per = (p.num_seqs + kThreads - 1) / kThreads, s0 = min(tid * per, p.num_seqs), s1 = min(s0 + per, p.num_seqs);
     const bool report = blockIdx.x == 0;
     int64_t sum = 0;
-    for (int s = s0; s < s1; ++s) sum += (int64_t)p.num_kv_heads * (kStartCost + int4_seq(p, s, report).n);
+    for (int s = s0; s < s1; ++s) sum += (int64_t)groups * (kStartCost + int4_seq(p, s, report).n);
     int64_t scan = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -670,20 +670,21 @@ __global__ void __launch_bounds__(kWarps * 32, int4_ctas_per_sm(RT))
     chunk_end[tid] = scan;
     __syncthreads();
     const int64_t total = chunk_end[kThreads - 1];
-    pdl_wait();
+    if (blockIdx.x == 0) pdl_wait();
     if (blockIdx.x == 0) {  // for the merge
         int64_t at = scan - sum;
         for (int s = s0; s < s1; ++s) {
             starts[s] = at;
-            at += (int64_t)p.num_kv_heads * (kStartCost + int4_seq(p, s, false).n);
+            at += (int64_t)groups * (kStartCost + int4_seq(p, s, false).n);
         }
         if (tid == 0) starts[p.num_seqs] = total;
         if (p.seq_order)  // results and shares do not depend on it; it is checked all the same
             for (int i = tid; i < p.num_seqs; i += kThreads) (void)scheduled_seq(p, i, true);
     }
     const int64_t me = (int64_t)blockIdx.x * kWarps + warp;
-    const int64_t share = int4_share(total, (int64_t)gridDim.x * kWarps);
-    int64_t x = me * share;
+    pdl_wait();
+    const int64_t share = int4_share(total, (int64_t)gridDim.x * kWarps >> team_bits);
+    int64_t x = (me >> team_bits) * share;
     const int64_t xend = min(x + share, total);
     if (x >= xend) return;
     // the sequence of place x: the thread whose run holds it, then its run
@@ -693,16 +694,17 @@ __global__ void __launch_bounds__(kWarps * 32, int4_ctas_per_sm(RT))
     int s = c * per;
     int64_t at = c == 0 ? 0 : chunk_end[c - 1];  // first place of sequence s
     Int4Seq seq = int4_seq(p, s, false);
-    while (x >= at + (int64_t)p.num_kv_heads * (kStartCost + seq.n)) {
-        at += (int64_t)p.num_kv_heads * (kStartCost + seq.n);
+    while (x >= at + (int64_t)groups * (kStartCost + seq.n)) {
+        at += (int64_t)groups * (kStartCost + seq.n);
         seq = int4_seq(p, ++s, false);
     }
-    int kvh = (int)((x - at) / (kStartCost + seq.n));
-    at += (int64_t)kvh * (kStartCost + seq.n);  // first place of (s, kvh)
+    int group = (int)((x - at) / (kStartCost + seq.n));
+    at += (int64_t)group * (kStartCost + seq.n);  // first place of (s, group)
     const int rows = p.group * p.q_len;
     T *out = reinterpret_cast<T *>(p.out);
     for (;;) {
         const int64_t blocks_at = at + kStartCost;
+        const int kvh = (group << team_bits) + member;
         const int from = (int)max((int64_t)0, x - blocks_at), to = (int)min((int64_t)seq.n, xend - blocks_at);
         if (seq.n == 0 && x <= at) {  // an empty context: zero rows
             for (int i = lane; i < rows * D; i += 32) out[query_row(p, s, kvh, i / D) * D + i % D] = E::from_float(0.f);
@@ -742,8 +744,8 @@ __global__ void __launch_bounds__(kWarps * 32, int4_ctas_per_sm(RT))
         at = blocks_at + seq.n;
         x = at;
         if (x >= xend) return;
-        if (++kvh == p.num_kv_heads) {
-            kvh = 0;
+        if (++group == groups) {
+            group = 0;
             seq = int4_seq(p, ++s, false);
         }
     }
@@ -754,7 +756,7 @@ __global__ void __launch_bounds__(kWarps * 32, int4_ctas_per_sm(RT))
 // of a sequence): kRowWarps warps share a row's pieces (1 where contexts have
 // few, 4 where they have many).
 template <typename T, int D, int kRowWarps>
-__global__ void __launch_bounds__(128) merge_int4_kernel(const DecodeParams p, const int64_t *starts, int64_t warps) {
+__global__ void __launch_bounds__(128) merge_int4_kernel(const DecodeParams p, const int64_t *starts, const int64_t warps, const int team_bits) {
     using E = Elem<T>;
     constexpr int kV = D / 32;
     __shared__ float red[4][D + 1];
@@ -766,12 +768,14 @@ __global__ void __launch_bounds__(128) merge_int4_kernel(const DecodeParams p, c
     const bool real = row < p.num_kv_heads * rows;
     const int kvh = real ? row / rows : 0, h = real ? row % rows : 0;
     pdl_wait();
-    const int64_t share = int4_share(starts[p.num_seqs], warps);
-    const int64_t at = starts[s] + (int64_t)kvh * (kStartCost + seq.n) + kStartCost;
+    const int64_t share = int4_share(starts[p.num_seqs], warps >> team_bits);
+    const int64_t at = starts[s] + (int64_t)(kvh >> team_bits) * (kStartCost + seq.n) + kStartCost;
     const int64_t wa = at / share, wb = (at + seq.n - 1) / share;
     const int pieces = seq.n == 0 || !real ? 0 : (int)(wb - wa + 1);
     if (kRowWarps == 4 ? pieces <= 1 : __all_sync(0xffffffffu, pieces <= 1)) return;  // written by its warp
-    auto slot = [&](int i) -> int64_t { return (i == 0 ? 2 * wa + 1 : 2 * (wa + i)) * rows + h; };
+    // piece i: the first in the second slot of its warp, the others in the first
+    const int member = kvh & ((1 << team_bits) - 1);
+    auto slot = [&](int i) -> int64_t { return (2 * (((wa + i) << team_bits) + member) + (i == 0 ? 1 : 0)) * rows + h; };
     float M = -INFINITY;
     for (int i = lane; i < pieces; i += 32) M = fmaxf(M, p.ws_lse[slot(i)]);
 #pragma unroll
@@ -849,15 +853,16 @@ cudaError_t launch_int4_t(const DecodeParams &p, int64_t *starts, int ctas, cuda
     static FuncAttrCache attrs;
     cudaError_t e = ensure_smem(kern, kSmem, attrs, /*max_carveout=*/true);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(kern, dim3(ctas), dim3(kWarps * 32), kSmem, stream, p, starts);
+    const int64_t warps = (int64_t)ctas * kWarps;
+    const int team_bits = p.num_kv_heads % 4 == 0 ? 2 : p.num_kv_heads % 2 == 0 ? 1 : 0;
+    e = launch_pdl(kern, dim3(ctas), dim3(kWarps * 32), kSmem, stream, p, starts, team_bits);
     if (e != cudaSuccess) return e;
     // pieces a context may have: many on few sequences
-    const int64_t warps = (int64_t)ctas * kWarps;
     const int rows = p.num_heads * p.q_len;
     const bool many = warps > 8 * (int64_t)p.num_seqs * p.num_kv_heads;
     const dim3 grid(many ? rows : (rows + 3) / 4, p.num_seqs);
-    return many ? launch_pdl(merge_int4_kernel<T, D, 4>, grid, dim3(128), 0, stream, p, (const int64_t *)starts, warps)
-                : launch_pdl(merge_int4_kernel<T, D, 1>, grid, dim3(128), 0, stream, p, (const int64_t *)starts, warps);
+    return many ? launch_pdl(merge_int4_kernel<T, D, 4>, grid, dim3(128), 0, stream, p, (const int64_t *)starts, warps, team_bits)
+                : launch_pdl(merge_int4_kernel<T, D, 1>, grid, dim3(128), 0, stream, p, (const int64_t *)starts, warps, team_bits);
 }
 
 template <typename T, int D>
