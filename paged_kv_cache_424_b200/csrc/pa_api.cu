@@ -81,8 +81,8 @@ struct Plan {
     size_t o_bytes = 0;    // partial outputs
     size_t lse_off = 0;    // offset of the lse array
     size_t ws_bytes = 0;   // total workspace (0 when unsplit)
-    int ctas = 0;          // 4-bit caches: CTAs of equal shares (0: partitions)
-    size_t starts_off = 0; // their prefix sums
+    int ctas = 0;          // 4-bit caches: CTAs of the shares (0: partitions)
+    size_t places_off = 0; // their prefix sums
 };
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -177,10 +177,13 @@ int tc_auto_partition(const pa_dims *d, int ctx_blocks, int rows, bool fp8) {
     return kAutoPartitionTc;
 }
 
-// Whether a 4-bit decode with automatic partitions cuts the batch into equal
-// shares of one wave of resident warps.  Short contexts and very many
-// sequences (every CTA adds up all lengths) take the partitioned kernel.
-bool int4_equal_shares(const pa_dims *d, int ctx_blocks) { return ctx_blocks > 8 && d->num_seqs <= 4096; }
+// Whether a 4-bit decode with automatic partitions cuts the batch into shares
+// for one wave of resident warps.  Short contexts and very many sequences
+// (every CTA adds up all lengths, in 31 bits) take the partitioned kernel.
+bool int4_shares(const pa_dims *d, int ctx_blocks) {
+    return ctx_blocks > 8 && d->num_seqs <= 4096 &&
+           (int64_t)d->num_seqs * d->num_kv_heads * (ctx_blocks + 64) < (int64_t)1 << 30;
+}
 
 pa_status make_plan(const pa_dims *d, int32_t max_context_len, int32_t partition_tokens, Plan *pl,
                     int32_t q_len = 1, int32_t window = 0) {
@@ -203,15 +206,15 @@ pa_status make_plan(const pa_dims *d, int32_t max_context_len, int32_t partition
     const int P = partition_tokens != 0 ? partition_tokens
                   : rows                ? tc_auto_partition(d, ctx_blocks, rows, kv_fp8(d))
                                         : kAutoPartitionSimt;
-    if (kv_int4(d) && partition_tokens == 0 && int4_equal_shares(d, ctx_blocks)) {
+    if (kv_int4(d) && partition_tokens == 0 && int4_shares(d, ctx_blocks)) {
         pl->ctas = pa::decode_int4_ctas(g * q_len, sm_count());
         pl->part_blocks = ctx_blocks;
         pl->max_parts = 1;
         const size_t wrows = (size_t)2 * pl->ctas * pa::kInt4Warps * g * q_len;
         pl->o_bytes = align_up(wrows * d->head_dim * sizeof(float), 256);
         pl->lse_off = pl->o_bytes;
-        pl->starts_off = pl->lse_off + align_up(wrows * sizeof(float), 256);
-        pl->ws_bytes = pl->starts_off + align_up(((size_t)d->num_seqs + 1) * sizeof(int64_t), 256);
+        pl->places_off = pl->lse_off + align_up(wrows * sizeof(float), 256);
+        pl->ws_bytes = pl->places_off + align_up(((size_t)d->num_seqs + 1) * sizeof(int32_t), 256);
         return PA_OK;
     }
     int part_blocks = P / 16;
@@ -280,8 +283,8 @@ pa_status decode_impl(void *out, const void *q, const void *k_cache, const void 
     const bool fp8 = kv_fp8(dims);
     if (kv_int4(dims)) {
         p.parts_per_cta = p.heads_per_cta = 1;
-        int64_t *starts = pl.ctas ? reinterpret_cast<int64_t *>(static_cast<char *>(workspace) + pl.starts_off) : nullptr;
-        const cudaError_t e = pa::launch_decode_int4(p, dims->dtype, dims->head_dim, g * q_len, starts, pl.ctas,
+        int32_t *places = pl.ctas ? reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + pl.places_off) : nullptr;
+        const cudaError_t e = pa::launch_decode_int4(p, dims->dtype, dims->head_dim, g * q_len, places, pl.ctas,
                                                      static_cast<cudaStream_t>(stream));
         return e == cudaSuccess ? PA_OK : cuda_fail(e, "pa_decode_int4 launch");
     }
@@ -410,7 +413,7 @@ int32_t pa_decode_num_partitions(const pa_dims *dims, int32_t max_context_len, i
     Plan pl;
     st = make_plan(dims, max_context_len, partition_tokens, &pl);
     if (st != PA_OK) return st;
-    // equal shares: at most one piece per warp, and one per 8 blocks of a context
+    // shares: at most one piece per warp, and one per 8 blocks of a context
     if (pl.ctas) return std::min(pl.ctas * pa::kInt4Warps, (pl.part_blocks + 7) / 8 + 1);
     return pl.max_parts;
 }

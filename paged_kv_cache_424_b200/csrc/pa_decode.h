@@ -98,13 +98,13 @@ bool decode_tc_supported(int head_dim, int rows, int64_t num_blocks, int num_kv_
 cudaError_t launch_decode_tc(const DecodeParams &p, int dtype, int rows, bool fp8_cache, cudaStream_t stream);
 
 // Decode over 4-bit caches for `rows` >= group * q_len query rows per KV head.
-// With `starts` (int64 [num_seqs + 1] in the workspace) the contexts are cut
-// into equal shares of `ctas` CTAs (decode_int4_ctas(rows, SMs); ws_o and ws_lse
-// hold two rows sets per warp, kInt4Warps warps per CTA); without, into the
-// partitions of p.
+// With `places` (int32 [num_seqs + 1] in the workspace) the contexts are cut
+// into equal shares for `ctas` CTAs (decode_int4_ctas(rows, SMs); ws_o
+// and ws_lse hold two sets of rows per warp, kInt4Warps warps per CTA); without,
+// into the partitions of p.
 constexpr int kInt4Warps = 4;
 int decode_int4_ctas(int rows, int sms);
-cudaError_t launch_decode_int4(const DecodeParams &p, int dtype, int head_dim, int rows, int64_t *starts, int ctas,
+cudaError_t launch_decode_int4(const DecodeParams &p, int dtype, int head_dim, int rows, int32_t *places, int ctas,
                                cudaStream_t stream);
 
 // Rotation of queries and keys, with or without the cache write.

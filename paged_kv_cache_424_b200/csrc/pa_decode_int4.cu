@@ -634,19 +634,19 @@ __device__ __forceinline__ Int4Seq int4_seq(const DecodeParams &p, int s, bool r
     return {sp.L, sp.bfirst, min(sp.nblk - sp.bfirst, p.part_blocks)};
 }
 
-__device__ __forceinline__ int64_t int4_share(int64_t total, int64_t warps) {
-    const int64_t w = (total + warps - 1) / warps;
-    return w < kMinShare ? kMinShare : w;
-}
+__device__ __forceinline__ int int4_share(int total, int teams) { return max(kMinShare, (total + teams - 1) / teams); }
 
+// places: int32 [num_seqs + 1] in the workspace, written for the merge: each
+// sequence's first place and the total.  (The host keeps totals that pass 30
+// bits off this kernel.)
 template <typename T, int D, int RT, bool kMasked>
 __global__ void __launch_bounds__(kWarps * 32, int4_ctas_per_sm(RT))
-    decode_int4_balanced_kernel(const DecodeParams p, int64_t *starts, const int team_bits) {
+    decode_int4_balanced_kernel(const DecodeParams p, int32_t *places, const int team_bits) {
     using E = Elem<T>;
     constexpr int kThreads = kWarps * 32;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ int64_t chunk_end[kThreads];
-    __shared__ int64_t warp_sum[kWarps];
+    __shared__ int64_t chunk_end[kThreads];  // 64-bit: with half the static shared memory the compiler's code for the
+    __shared__ int64_t warp_sum[kWarps];     // loop over blocks came out slower (7B batch 62 us against 69)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, q = lane & 3;
     pdl_launch_dependents();
     const uint32_t ring = smem_addr(smem) + warp * kStages * 4 * int4_chunk_bytes(D);
@@ -656,56 +656,57 @@ __global__ void __launch_bounds__(kWarps * 32, int4_ctas_per_sm(RT))
     // writes lengths)
     const int per = (p.num_seqs + kThreads - 1) / kThreads, s0 = min(tid * per, p.num_seqs), s1 = min(s0 + per, p.num_seqs);
     const bool report = blockIdx.x == 0;
-    int64_t sum = 0;
-    for (int s = s0; s < s1; ++s) sum += (int64_t)groups * (kStartCost + int4_seq(p, s, report).n);
-    int64_t scan = sum;
+    int sum = 0;
+    for (int s = s0; s < s1; ++s) sum += groups * (kStartCost + int4_seq(p, s, report).n);
+    int scan = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, scan, o);
+        const int v = __shfl_up_sync(0xffffffffu, scan, o);
         if (lane >= o) scan += v;
     }
     if (lane == 31) warp_sum[warp] = scan;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) scan += warp_sum[w];
+    for (int w = 0; w < warp; ++w) scan += (int)warp_sum[w];
     chunk_end[tid] = scan;
     __syncthreads();
-    const int64_t total = chunk_end[kThreads - 1];
-    if (blockIdx.x == 0) pdl_wait();
-    if (blockIdx.x == 0) {  // for the merge
-        int64_t at = scan - sum;
+    const int total = (int)chunk_end[kThreads - 1];
+    const int teams = ((int)gridDim.x * kWarps) >> team_bits, share = int4_share(total, teams);
+    if (blockIdx.x == 0) {
+        pdl_wait();  // an earlier call's merge may still read them
+        int at = scan - sum;
         for (int s = s0; s < s1; ++s) {
-            starts[s] = at;
-            at += (int64_t)groups * (kStartCost + int4_seq(p, s, false).n);
+            places[s] = at;
+            at += groups * (kStartCost + int4_seq(p, s, false).n);
         }
-        if (tid == 0) starts[p.num_seqs] = total;
+        if (tid == 0) places[p.num_seqs] = total;
         if (p.seq_order)  // results and shares do not depend on it; it is checked all the same
             for (int i = tid; i < p.num_seqs; i += kThreads) (void)scheduled_seq(p, i, true);
     }
-    const int64_t me = (int64_t)blockIdx.x * kWarps + warp;
+    const int me = (int)blockIdx.x * kWarps + warp;
+    const int64_t begin = (int64_t)(me >> team_bits) * share;
+    int x = (int)min((int64_t)total, begin);
+    const int xend = (int)min((int64_t)total, begin + share);
     pdl_wait();
-    const int64_t share = int4_share(total, (int64_t)gridDim.x * kWarps >> team_bits);
-    int64_t x = (me >> team_bits) * share;
-    const int64_t xend = min(x + share, total);
     if (x >= xend) return;
     // the sequence of place x: the thread whose run holds it, then its run
     int c = 0;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) c += __popc(__ballot_sync(0xffffffffu, chunk_end[32 * i + lane] <= x));
     int s = c * per;
-    int64_t at = c == 0 ? 0 : chunk_end[c - 1];  // first place of sequence s
+    int at = c == 0 ? 0 : (int)chunk_end[c - 1];  // first place of sequence s
     Int4Seq seq = int4_seq(p, s, false);
-    while (x >= at + (int64_t)groups * (kStartCost + seq.n)) {
-        at += (int64_t)groups * (kStartCost + seq.n);
+    while (x >= at + groups * (kStartCost + seq.n)) {
+        at += groups * (kStartCost + seq.n);
         seq = int4_seq(p, ++s, false);
     }
-    int group = (int)((x - at) / (kStartCost + seq.n));
-    at += (int64_t)group * (kStartCost + seq.n);  // first place of (s, group)
+    int group = (x - at) / (kStartCost + seq.n);
+    at += group * (kStartCost + seq.n);  // first place of (s, group)
     const int rows = p.group * p.q_len;
     T *out = reinterpret_cast<T *>(p.out);
     for (;;) {
-        const int64_t blocks_at = at + kStartCost;
+        const int blocks_at = at + kStartCost;
         const int kvh = (group << team_bits) + member;
-        const int from = (int)max((int64_t)0, x - blocks_at), to = (int)min((int64_t)seq.n, xend - blocks_at);
+        const int from = max(0, x - blocks_at), to = min(seq.n, xend - blocks_at);
         if (seq.n == 0 && x <= at) {  // an empty context: zero rows
             for (int i = lane; i < rows * D; i += 32) out[query_row(p, s, kvh, i / D) * D + i % D] = E::from_float(0.f);
         } else if (to > from) {
@@ -714,7 +715,7 @@ __global__ void __launch_bounds__(kWarps * 32, int4_ctas_per_sm(RT))
             w.run(p, ring, span, lane);
             w.finish();
             const bool all = from == 0 && to == seq.n;
-            const int64_t slot = 2 * me + (from == 0 ? 1 : 0);  // the context's first piece, or a later one
+            const int64_t slot = 2 * (int64_t)me + (from == 0 ? 1 : 0);  // the context's first piece, or a later one
 #pragma unroll
             for (int n = 0; n < RT; ++n) {
                 const int h = 4 * n + q;
@@ -756,7 +757,7 @@ __global__ void __launch_bounds__(kWarps * 32, int4_ctas_per_sm(RT))
 // of a sequence): kRowWarps warps share a row's pieces (1 where contexts have
 // few, 4 where they have many).
 template <typename T, int D, int kRowWarps>
-__global__ void __launch_bounds__(128) merge_int4_kernel(const DecodeParams p, const int64_t *starts, const int64_t warps, const int team_bits) {
+__global__ void __launch_bounds__(128) merge_int4_kernel(const DecodeParams p, const int32_t *places, const int teams, const int team_bits) {
     using E = Elem<T>;
     constexpr int kV = D / 32;
     __shared__ float red[4][D + 1];
@@ -768,47 +769,44 @@ __global__ void __launch_bounds__(128) merge_int4_kernel(const DecodeParams p, c
     const bool real = row < p.num_kv_heads * rows;
     const int kvh = real ? row / rows : 0, h = real ? row % rows : 0;
     pdl_wait();
-    const int64_t share = int4_share(starts[p.num_seqs], warps >> team_bits);
-    const int64_t at = starts[s] + (int64_t)(kvh >> team_bits) * (kStartCost + seq.n) + kStartCost;
-    const int64_t wa = at / share, wb = (at + seq.n - 1) / share;
-    const int pieces = seq.n == 0 || !real ? 0 : (int)(wb - wa + 1);
+    const int share = int4_share(places[p.num_seqs], teams);
+    const int at = places[s] + (kvh >> team_bits) * (kStartCost + seq.n) + kStartCost;
+    const int ta = at / share;
+    const int pieces = seq.n == 0 || !real ? 0 : (at + seq.n - 1) / share - ta + 1;
     if (kRowWarps == 4 ? pieces <= 1 : __all_sync(0xffffffffu, pieces <= 1)) return;  // written by its warp
     // piece i: the first in the second slot of its warp, the others in the first
     const int member = kvh & ((1 << team_bits) - 1);
-    auto slot = [&](int i) -> int64_t { return (2 * (((wa + i) << team_bits) + member) + (i == 0 ? 1 : 0)) * rows + h; };
+    auto slot = [&](int i) -> int64_t { return (2 * (((int64_t)(ta + i) << team_bits) + member) + (i == 0 ? 1 : 0)) * rows + h; };
     float M = -INFINITY;
     for (int i = lane; i < pieces; i += 32) M = fmaxf(M, p.ws_lse[slot(i)]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     float acc[kV] = {}, wsum = 0.f;
-    if (M != -INFINITY) {
-        constexpr int kInFlight = 4;
-        for (int i0 = warp % kRowWarps; i0 < pieces; i0 += kRowWarps * kInFlight) {
-            float w[kInFlight], v[kInFlight][kV];
+    constexpr int kInFlight = 4;
+    bool first = true;
+    for (int i0 = warp % kRowWarps; i0 < pieces || first; i0 += kRowWarps * kInFlight) {
+        float lse[kInFlight], v[kInFlight][kV];
 #pragma unroll
-            for (int k = 0; k < kInFlight; ++k) {
-                const int i = i0 + k * kRowWarps;
-                const float lse = i < pieces ? p.ws_lse[slot(i)] : -INFINITY;
-                w[k] = 0.f;
+        for (int k = 0; k < kInFlight; ++k) {  // every piece was written: no need to look at its lse first
+            const int i = i0 + k * kRowWarps;
+            lse[k] = i < pieces ? p.ws_lse[slot(i)] : -INFINITY;
 #pragma unroll
-                for (int e = 0; e < kV; ++e) v[k][e] = 0.f;
-                if (lse != -INFINITY) {
-                    w[k] = exp2f(lse - M);
-                    const float *src = p.ws_o + slot(i) * D + lane * kV;
-#pragma unroll
-                    for (int e = 0; e < kV; e += 2) {
-                        const float2 f = *reinterpret_cast<const float2 *>(src + e);
-                        v[k][e] = f.x;
-                        v[k][e + 1] = f.y;
-                    }
-                }
+            for (int e = 0; e < kV; e += 2) {
+                const float2 f = i < pieces ? *reinterpret_cast<const float2 *>(p.ws_o + slot(i) * D + lane * kV + e)
+                                            : make_float2(0.f, 0.f);
+                v[k][e] = f.x;
+                v[k][e + 1] = f.y;
             }
+        }
+        if (first) {
 #pragma unroll
-            for (int k = 0; k < kInFlight; ++k) {
-                wsum += w[k];
+            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+            first = false;
+        }
 #pragma unroll
-                for (int e = 0; e < kV; ++e) acc[e] = fmaf(w[k], v[k][e], acc[e]);
-            }
+        for (int k = 0; k < kInFlight; ++k) {
+            const float w = lse[k] == -INFINITY ? 0.f : exp2f(lse[k] - M);
+            wsum += w;
+#pragma unroll
+            for (int e = 0; e < kV; ++e) acc[e] = fmaf(w, v[k][e], acc[e]);
         }
     }
     if constexpr (kRowWarps == 4) {
@@ -838,9 +836,9 @@ __global__ void __launch_bounds__(128) merge_int4_kernel(const DecodeParams p, c
 }
 
 template <typename T, int D, int RT, bool kMasked>
-cudaError_t launch_int4_t(const DecodeParams &p, int64_t *starts, int ctas, cudaStream_t stream) {
+cudaError_t launch_int4_t(const DecodeParams &p, int32_t *places, int ctas, cudaStream_t stream) {
     constexpr int kSmem = Int4Layout(D, 4 * RT).bytes;
-    if (!starts) {
+    if (!places) {
         auto kern = decode_int4_kernel<T, D, RT, kMasked>;
         static FuncAttrCache attrs;
         cudaError_t e = ensure_smem(kern, kSmem, attrs, /*max_carveout=*/true);
@@ -853,25 +851,25 @@ cudaError_t launch_int4_t(const DecodeParams &p, int64_t *starts, int ctas, cuda
     static FuncAttrCache attrs;
     cudaError_t e = ensure_smem(kern, kSmem, attrs, /*max_carveout=*/true);
     if (e != cudaSuccess) return e;
-    const int64_t warps = (int64_t)ctas * kWarps;
     const int team_bits = p.num_kv_heads % 4 == 0 ? 2 : p.num_kv_heads % 2 == 0 ? 1 : 0;
-    e = launch_pdl(kern, dim3(ctas), dim3(kWarps * 32), kSmem, stream, p, starts, team_bits);
+    const int teams = (ctas * kWarps) >> team_bits;
+    e = launch_pdl(kern, dim3(ctas), dim3(kWarps * 32), kSmem, stream, p, places, team_bits);
     if (e != cudaSuccess) return e;
     // pieces a context may have: many on few sequences
     const int rows = p.num_heads * p.q_len;
-    const bool many = warps > 8 * (int64_t)p.num_seqs * p.num_kv_heads;
+    const bool many = (int64_t)ctas * kWarps > 8 * (int64_t)p.num_seqs * p.num_kv_heads;
     const dim3 grid(many ? rows : (rows + 3) / 4, p.num_seqs);
-    return many ? launch_pdl(merge_int4_kernel<T, D, 4>, grid, dim3(128), 0, stream, p, (const int64_t *)starts, warps, team_bits)
-                : launch_pdl(merge_int4_kernel<T, D, 1>, grid, dim3(128), 0, stream, p, (const int64_t *)starts, warps, team_bits);
+    return many ? launch_pdl(merge_int4_kernel<T, D, 4>, grid, dim3(128), 0, stream, p, (const int32_t *)places, teams, team_bits)
+                : launch_pdl(merge_int4_kernel<T, D, 1>, grid, dim3(128), 0, stream, p, (const int32_t *)places, teams, team_bits);
 }
 
 template <typename T, int D>
-cudaError_t launch_int4_d(const DecodeParams &p, int rows, int64_t *starts, int ctas, cudaStream_t stream) {
+cudaError_t launch_int4_d(const DecodeParams &p, int rows, int32_t *places, int ctas, cudaStream_t stream) {
     const bool masked = decode_masked(p);
     switch (int4_row_tiles(rows)) {
-        case 1: return masked ? launch_int4_t<T, D, 1, true>(p, starts, ctas, stream) : launch_int4_t<T, D, 1, false>(p, starts, ctas, stream);
-        case 2: return masked ? launch_int4_t<T, D, 2, true>(p, starts, ctas, stream) : launch_int4_t<T, D, 2, false>(p, starts, ctas, stream);
-        default: return masked ? launch_int4_t<T, D, 4, true>(p, starts, ctas, stream) : launch_int4_t<T, D, 4, false>(p, starts, ctas, stream);
+        case 1: return masked ? launch_int4_t<T, D, 1, true>(p, places, ctas, stream) : launch_int4_t<T, D, 1, false>(p, places, ctas, stream);
+        case 2: return masked ? launch_int4_t<T, D, 2, true>(p, places, ctas, stream) : launch_int4_t<T, D, 2, false>(p, places, ctas, stream);
+        default: return masked ? launch_int4_t<T, D, 4, true>(p, places, ctas, stream) : launch_int4_t<T, D, 4, false>(p, places, ctas, stream);
     }
 }
 
@@ -879,13 +877,13 @@ cudaError_t launch_int4_d(const DecodeParams &p, int rows, int64_t *starts, int 
 
 int decode_int4_ctas(int rows, int sms) { return sms * int4_ctas_per_sm(int4_row_tiles(rows)); }
 
-cudaError_t launch_decode_int4(const DecodeParams &p, int dtype, int head_dim, int rows, int64_t *starts, int ctas,
+cudaError_t launch_decode_int4(const DecodeParams &p, int dtype, int head_dim, int rows, int32_t *places, int ctas,
                                cudaStream_t stream) {
     if (dtype == PA_F16)
-        return head_dim == 64 ? launch_int4_d<__half, 64>(p, rows, starts, ctas, stream)
-                              : launch_int4_d<__half, 128>(p, rows, starts, ctas, stream);
-    return head_dim == 64 ? launch_int4_d<__nv_bfloat16, 64>(p, rows, starts, ctas, stream)
-                          : launch_int4_d<__nv_bfloat16, 128>(p, rows, starts, ctas, stream);
+        return head_dim == 64 ? launch_int4_d<__half, 64>(p, rows, places, ctas, stream)
+                              : launch_int4_d<__half, 128>(p, rows, places, ctas, stream);
+    return head_dim == 64 ? launch_int4_d<__nv_bfloat16, 64>(p, rows, places, ctas, stream)
+                          : launch_int4_d<__nv_bfloat16, 128>(p, rows, places, ctas, stream);
 }
 
 }  // namespace pa
