@@ -354,6 +354,7 @@ pa_status check_rope(const pa_dims *d, const pa_rope_opts *r) {
 pa_status fill_rope(pa::RopeParams *p, void *q_out, const void *q, void *k_out, const void *k, const void *v,
                     const int64_t *positions, int32_t num_tokens, const pa_dims *d, const pa_rope_opts *r,
                     int64_t q_stride, int64_t k_stride, int64_t v_stride) {
+    if (d->num_heads > 65535 || d->num_kv_heads > 65535) return fail(PA_ERR_SHAPE, "num_heads and num_kv_heads must be <= 65535");
     const int64_t qrow = (int64_t)d->num_heads * d->head_dim, krow = (int64_t)d->num_kv_heads * d->head_dim;
     pa_status st;
     if (q && (st = check_stride("q_stride", q_stride, qrow)) != PA_OK) return st;

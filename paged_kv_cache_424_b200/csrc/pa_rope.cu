@@ -6,11 +6,12 @@
 //   a' = m (a cos - b sin),  b' = m (b cos + a sin).
 // All of it is data movement: each element is read once and written once.
 //
-// CTA = one token.  Its first rotary_dim / 2 threads compute the token's
-// (m cos, m sin) pairs in fp64 and share them through shared memory, so the
-// sines are computed once per token and not once per head.  Then D / 8 lanes
-// take a row (a head's D elements): 16 bytes per lane, the partner elements
-// of a pair by a shuffle.
+// CTA = one token (or some of its rows, when there are few tokens).  Its first
+// rotary_dim / 2 threads compute the token's (m cos, m sin) pairs in fp64 and
+// share them through shared memory, so the sines are computed once per token
+// and not once per head.  Then D / 8 lanes take a row (a head's D elements): 16
+// bytes per lane, the partner elements of a pair by a shuffle, the next pass's
+// rows in flight while one is worked on.
 #include "pa_common.cuh"
 #include "pa_decode.h"
 #include "pa_int4.cuh"
@@ -20,7 +21,8 @@ namespace pa {
 namespace {
 
 constexpr int kBlock = 16;
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;       // of the rotating kernel
+constexpr int kGatherThreads = 256;
 constexpr int kMaxHalf = 64;  // rotary_dim / 2 at most
 
 // Cache kinds of the templates below.
@@ -79,6 +81,109 @@ __device__ __forceinline__ uint4 narrow8(const float (&x)[8]) {
     return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
+__device__ __forceinline__ uint64_t pk2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 up2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+// Two single-precision operations in one instruction, each rounded by itself.
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// x / b for two x, correctly rounded, from y = RN(1 / b): q = RN(x y), r = x - b
+// q (exact), RN(q + r y).  That is the quotient whenever b's significand is not
+// all ones and nothing leaves the normal range (P. Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990); the
+// callers keep b between 2^-80 and 2^100 for quotients that matter.
+__device__ __forceinline__ uint64_t divide2(uint64_t x, uint64_t y, uint64_t minus_b) {
+    const uint64_t q = mul2(x, y);
+    return fma2(fma2(minus_b, q, x), y, q);
+}
+__device__ __forceinline__ bool divide2_fits(float b) {
+    return fabsf(b) > 0x1p-80f && fabsf(b) < 0x1p100f && (__float_as_uint(b) & 0x7fffffu) != 0x7fffffu;
+}
+
+// The 4-bit codes of 8 elements (element i in bits 4 i ..): round_half_even((x
+// - low) / sc) clamped to 0..15, the quotient rounded to fp32 first.  sc is
+// finite and not 0.
+__device__ __forceinline__ uint32_t int4_codes(const float (&x)[8], float low, float sc) {
+    constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer, half to even
+    uint32_t codes = 0;
+    if (divide2_fits(sc)) {
+        const float inv = __frcp_rn(sc);
+        const uint64_t y = pk2(inv, inv), mb = pk2(-sc, -sc), ml = pk2(-low, -low), magic = pk2(kRound, kRound);
+#pragma unroll
+        for (int i = 6; i >= 0; i -= 2) {
+            const float2 k = up2(add2(divide2(add2(pk2(x[i], x[i + 1]), ml), y, mb), magic));
+            const float k0 = fminf(fmaxf(k.x, kRound), kRound + 15.f), k1 = fminf(fmaxf(k.y, kRound), kRound + 15.f);
+            // the low bits of k are the integer: Horner in base 16, the constant part taken off at the end
+            codes = (codes * 16u + __float_as_uint(k1)) * 16u + __float_as_uint(k0);
+        }
+        return codes - 0x4b400000u * 0x11111111u;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float u = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[i], low), sc)), 0.f), 15.f);
+        codes |= (uint32_t)u << (4 * i);
+    }
+    return codes;
+}
+
+// E4M3 codes of x / scale (nearest, ties to even, clamped to 448, NaN kept).
+__device__ __forceinline__ uint2 e4m3_codes(const float (&x)[8], float scale) {
+    uint32_t u[2];
+    if (divide2_fits(scale)) {
+        const float inv = __frcp_rn(scale), most = 512.f * scale;  // beyond it every quotient is clamped
+        const uint64_t y = pk2(inv, inv), mb = pk2(-scale, -scale);
+        uint16_t h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = min_nan(max_nan(x[2 * i], -most), most), b = min_nan(max_nan(x[2 * i + 1], -most), most);
+            const float2 q = up2(divide2(pk2(a, b), y, mb));
+            h[i] = float2_to_e4m3x2(q.x, q.y);
+        }
+        u[0] = (uint32_t)h[0] | ((uint32_t)h[1] << 16);
+        u[1] = (uint32_t)h[2] | ((uint32_t)h[3] << 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t lo = float2_to_e4m3x2(__fdiv_rn(x[4 * i], scale), __fdiv_rn(x[4 * i + 1], scale));
+            const uint32_t hi = float2_to_e4m3x2(__fdiv_rn(x[4 * i + 2], scale), __fdiv_rn(x[4 * i + 3], scale));
+            u[i] = lo | (hi << 16);
+        }
+    }
+    return make_uint2(u[0], u[1]);
+}
+
 // The row of `slot` and KV head h takes the 8 elements x (dims 8 c ..) of
 // each of the row's LPR lanes (all of them converged; `live`: this lane's
 // row is written).
@@ -92,30 +197,19 @@ __device__ __forceinline__ void store_row(void *cache, const float (&x)[8], int6
     if constexpr (kCache == kCache16) {
         if (live) reinterpret_cast<uint4 *>(cache)[(chunk * kBlock + off) * LPR + c] = narrow8<T>(x);
     } else if constexpr (kCache == kCacheE4m3) {
-        if (live) {
-            uint32_t u[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint32_t lo = float2_to_e4m3x2(__fdiv_rn(x[4 * i], scale), __fdiv_rn(x[4 * i + 1], scale));
-                const uint32_t hi = float2_to_e4m3x2(__fdiv_rn(x[4 * i + 2], scale), __fdiv_rn(x[4 * i + 3], scale));
-                u[i] = lo | (hi << 16);
-            }
-            reinterpret_cast<uint2 *>(cache)[(chunk * kBlock + off) * LPR + c] = make_uint2(u[0], u[1]);
-        }
+        if (live) reinterpret_cast<uint2 *>(cache)[(chunk * kBlock + off) * LPR + c] = e4m3_codes(x, scale);
     } else if constexpr (kCache == kCacheInt4) {
+        // a NaN goes through both; an infinity makes the range infinite or NaN
         float lo = x[0], hi = x[0];
-        bool fine = true;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            lo = fminf(lo, x[i]);
-            hi = fmaxf(hi, x[i]);
-            fine = fine && fabsf(x[i]) < INFINITY;  // false for NaN too
+        for (int i = 1; i < 8; ++i) {
+            lo = min_nan(lo, x[i]);
+            hi = max_nan(hi, x[i]);
         }
-        if (!fine) hi = INFINITY;
 #pragma unroll
         for (int o = LPR / 2; o > 0; o >>= 1) {
-            lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+            lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+            hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
         }
         if (!live) return;
         __nv_bfloat16 lb = __float2bfloat16_rn(lo);
@@ -123,15 +217,10 @@ __device__ __forceinline__ void store_row(void *cache, const float (&x)[8], int6
         __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(__fsub_rn(hi, low), 15.f));
         const float sc = __bfloat162float(sb);
         uint32_t codes = 0;
-        if (!(fabsf(sc) < INFINITY)) {  // a NaN or an infinity in the row, or a range past fp32's
+        if (!(fabsf(sc) < INFINITY))  // a NaN or an infinity in the row, or a range past fp32's
             lb = sb = __float2bfloat16_rn(NAN);
-        } else if (sc != 0.f) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float u = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[i], low), sc)), 0.f), 15.f);
-                codes |= (uint32_t)u << (4 * i);
-            }
-        }
+        else if (sc != 0.f)
+            codes = int4_codes(x, low, sc);
         unsigned char *base = reinterpret_cast<unsigned char *>(cache) + chunk * int4_chunk_bytes(D);
         *reinterpret_cast<uint32_t *>(base + off * (D / 2) + c * 4) = codes;
         if (c == 0) {
@@ -141,175 +230,288 @@ __device__ __forceinline__ void store_row(void *cache, const float (&x)[8], int6
     }
 }
 
-template <typename T, int D, int kCache>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
-    constexpr int LPR = D / 8;        // lanes per row
-    constexpr int RPW = 32 / LPR;     // rows per warp
-    __shared__ __align__(16) float2 cs[kMaxHalf];
-    const int t = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+constexpr int kWave = 148 * 7;  // CTAs that a device holds at once
+
+// How a row's pairs lie in its lanes' 8 dims.
+enum { kPairsNone = 0, kPairsHalf = 1, kPairsInterleaved = 2, kPairsHalfOdd = 3 };  // kPairsHalf: rotary_dim / 2 a multiple of 8
+
+// CTA = tokens blockIdx.x, blockIdx.x + gridDim.x, ...; of each the passes
+// blockIdx.y, blockIdx.y + gridDim.y, ... over its rows, 2 kRows rows each.
+template <typename T, int D, int kCache, int kPairs>
+__global__ void __launch_bounds__(kThreads, 7) rope_kernel(const RopeParams p) {
+    constexpr int LPR = D / 8;             // lanes per row
+    constexpr int kRows = kThreads / LPR;  // rows that the CTA's lanes hold at once
+    __shared__ __align__(16) float2 cs_s[2][kMaxHalf];
+    const int tid = threadIdx.x, lane = tid & 31;
     // The decode kernels read q before they wait for the kernel in front of
     // them, so a kernel that writes q or k does not let the next one start
     // early; a cache write alone does.
     if (!p.q_out && !p.k_out) pdl_launch_dependents();
-    pdl_wait();
-    int64_t slot = 0;
-    if constexpr (kCache != kCacheNone) {
-        slot = p.slots[t];
-        if (slot < 0) return;  // padding token
-    }
     const int half = p.half;
-    if (tid < half) {
-        double s, c;
-        sincos_turns((double)p.positions[t] * p.inv_freq[tid] * 0.15915494309189533576888, &s, &c);
-        if (p.inverse) s = -s;
-        cs[tid] = make_float2((float)(c * p.magnitude), (float)(s * p.magnitude));
-    }
-    __syncthreads();
-    bool slot_ok = true;
-    if constexpr (kCache != kCacheNone) {
-        slot_ok = slot < p.num_slots;
-        if (!slot_ok && tid == 0) flag_error(PA_DEVERR_SLOT);
-    }
     const int c = lane % LPR, d0 = 8 * c;  // this lane's dims d0 .. d0 + 7
     const int H = p.num_heads, Hk = p.num_kv_heads;
     const int total = H + (kCache == kCacheNone ? Hk : 2 * Hk);
-    for (int base = warp * RPW; base < total; base += (kThreads / 32) * RPW) {
-        const int row = base + lane / LPR;
-        const bool valid = row < total;
-        const bool is_q = row < H, is_v = row >= H + Hk;
-        const int h = is_q ? row : is_v ? row - H - Hk : row - H;
-        const T *src = is_q ? reinterpret_cast<const T *>(p.q) + t * p.q_stride
-                       : is_v ? reinterpret_cast<const T *>(p.v) + t * p.v_stride
-                              : reinterpret_cast<const T *>(p.k) + t * p.k_stride;
-        src += (int64_t)h * D;
-        float x[8];
-        {
-            const uint4 w = valid ? *reinterpret_cast<const uint4 *>(src + d0) : make_uint4(0, 0, 0, 0);
-            widen8<T>(w, x);
-        }
-        const bool turn = valid && !is_v;
-        float y[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = x[i];
-        if (p.interleaved) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (turn && 4 * c + i < half) {
-                    const float2 k = cs[4 * c + i];
-                    y[2 * i] = __fsub_rn(__fmul_rn(x[2 * i], k.x), __fmul_rn(x[2 * i + 1], k.y));
-                    y[2 * i + 1] = __fadd_rn(__fmul_rn(x[2 * i + 1], k.x), __fmul_rn(x[2 * i], k.y));
-                }
-            }
-        } else {
-            float o[8];  // the pair's other element
-            if (half % 8 == 0) {
-                const int step = half / 8;
-                const int other = lane - c + (c < step ? c + step : c < 2 * step ? c - step : c);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = __shfl_sync(0xffffffffu, x[i], other);
-            } else {
-                // pairs that straddle the lanes' 8 dims: single elements, all
-                // read before the row is written (it may be written in place)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int d = d0 + i;
-                    o[i] = turn && d < 2 * half ? Elem<T>::to_float(src[d < half ? d + half : d - half]) : 0.f;
-                }
-                __syncwarp();
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int d = d0 + i;
-                if (turn && d < 2 * half) {
-                    const float2 k = cs[d < half ? d : d - half];
-                    const float a = __fmul_rn(x[i], k.x), b = __fmul_rn(o[i], k.y);
-                    y[i] = d < half ? __fsub_rn(a, b) : __fadd_rn(a, b);
-                }
+    const int first = (int)blockIdx.y * 2 * kRows, step = 2 * kRows * (int)gridDim.y;  // of the CTA's passes
+    const int mine = tid / LPR;                                                        // this lane's row in a pass
+    // positions, slots and frequencies are no kernel of this library's output:
+    // the first token's sines are computed before the wait for the kernel in
+    // front, a later one's while the token before it is worked on
+    const double freq = kPairs != kPairsNone && tid < half ? p.inv_freq[tid] * 0.15915494309189533576888 : 0.0;
+    auto sines = [&](int t, int buf) {
+        if constexpr (kPairs != kPairsNone) {
+            if (tid < half) {
+                double s, co;
+                sincos_turns((double)p.positions[t] * freq, &s, &co);
+                if (p.inverse) s = -s;
+                cs_s[buf][tid] = make_float2((float)(co * p.magnitude), (float)(s * p.magnitude));
             }
         }
-        if (is_q) {
-            if (valid) *reinterpret_cast<uint4 *>(reinterpret_cast<T *>(p.q_out) + ((int64_t)t * H + h) * D + d0) = narrow8<T>(y);
-        } else if constexpr (kCache == kCacheNone) {
-            if (valid) *reinterpret_cast<uint4 *>(reinterpret_cast<T *>(p.k_out) + ((int64_t)t * Hk + h) * D + d0) = narrow8<T>(y);
+    };
+    auto slot_of = [&](int t) -> int64_t { return kCache == kCacheNone ? 0 : p.slots[t]; };
+    auto load = [&](int t, int row) -> uint4 {  // queries, keys, values in this order
+        if (row >= total) return make_uint4(0, 0, 0, 0);
+        const T *base = row < H ? reinterpret_cast<const T *>(p.q)
+                        : row < H + Hk ? reinterpret_cast<const T *>(p.k) : reinterpret_cast<const T *>(p.v);
+        const int64_t stride = row < H ? p.q_stride : row < H + Hk ? p.k_stride : p.v_stride;
+        const int h = row < H ? row : row < H + Hk ? row - H : row - H - Hk;
+        return *reinterpret_cast<const uint4 *>(base + t * stride + (h * D + d0));
+    };
+    int t = blockIdx.x, buf = 0;
+    int64_t slot = slot_of(t);
+    if (slot >= 0) sines(t, 0);
+    pdl_wait();
+    uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (slot >= 0) {
+        w[0] = load(t, first + mine);
+        w[1] = load(t, first + mine + kRows);
+    }
+    for (;;) {
+        const int t2 = t + (int)gridDim.x;
+        const bool more = t2 < p.num_tokens;
+        const int64_t slot2 = more ? slot_of(t2) : -1;
+        if constexpr (kPairs != kPairsNone) __syncthreads();  // this token's sines are there, those of the one before are done with
+        if (more && slot2 >= 0) sines(t2, buf ^ 1);
+        const bool slot_ok = kCache == kCacheNone || slot < p.num_slots;
+        if (!slot_ok && tid == 0 && blockIdx.y == 0) flag_error(PA_DEVERR_SLOT);
+        const float2 *cs = cs_s[buf];
+        // a token with a negative slot is padding: nothing of it is read or written
+        // (the loop's bounds are the CTA's: every lane of a warp stays in it)
+        for (int pass = slot < 0 ? total : first; pass < total; pass += step) {
+            const int row0 = pass + mine;
+            uint4 w2[2];  // the next pass's rows, or the next token's
+            const bool last = pass + step >= total;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                w2[u] = !last ? load(t, row0 + step + u * kRows)
+                        : slot2 >= 0 ? load(t2, first + mine + u * kRows) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int row = row0 + u * kRows;
+                const bool valid = row < total, is_q = row < H, is_v = row >= H + Hk;
+                const int h = is_q ? row : is_v ? row - H - Hk : row - H;
+                float x[8];
+                widen8<T>(w[u], x);
+                if constexpr (kPairs == kPairsInterleaved) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (valid && !is_v && 4 * c + i < half) {
+                            const float2 k = cs[4 * c + i];
+                            const float a = x[2 * i], b = x[2 * i + 1];
+                            x[2 * i] = __fsub_rn(__fmul_rn(a, k.x), __fmul_rn(b, k.y));
+                            x[2 * i + 1] = __fadd_rn(__fmul_rn(b, k.x), __fmul_rn(a, k.y));
+                        }
+                    }
+                } else if constexpr (kPairs == kPairsHalf) {
+                    const int q8 = half / 8;  // lanes of a half
+                    const int other = lane - c + (c < q8 ? c + q8 : c < 2 * q8 ? c - q8 : c);
+                    uint4 wo;
+                    wo.x = __shfl_sync(0xffffffffu, w[u].x, other);
+                    wo.y = __shfl_sync(0xffffffffu, w[u].y, other);
+                    wo.z = __shfl_sync(0xffffffffu, w[u].z, other);
+                    wo.w = __shfl_sync(0xffffffffu, w[u].w, other);
+                    if (valid && !is_v && c < 2 * q8) {
+                        // a' = a cos + (-b) sin, b' = b cos + a sin
+                        const uint32_t sign = c < q8 ? 0x80008000u : 0u;
+                        wo = make_uint4(wo.x ^ sign, wo.y ^ sign, wo.z ^ sign, wo.w ^ sign);
+                        float o[8];
+                        widen8<T>(wo, o);
+                        const float4 *k = reinterpret_cast<const float4 *>(cs + (c < q8 ? d0 : d0 - half));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float4 f = k[i];  // (cos, sin) of two pairs
+                            const float2 y = up2(add2(mul2(pk2(x[2 * i], x[2 * i + 1]), pk2(f.x, f.z)),
+                                                      mul2(pk2(o[2 * i], o[2 * i + 1]), pk2(f.y, f.w))));
+                            x[2 * i] = y.x;
+                            x[2 * i + 1] = y.y;
+                        }
+                    }
+                } else if constexpr (kPairs == kPairsHalfOdd) {
+                    // pairs that straddle the lanes' 8 dims: single elements, all
+                    // read before the row is written (it may be written in place)
+                    float o[8];
+                    const T *src = is_q ? reinterpret_cast<const T *>(p.q) + t * p.q_stride + h * D
+                                        : reinterpret_cast<const T *>(p.k) + t * p.k_stride + h * D;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int d = d0 + i;
+                        o[i] = valid && !is_v && d < 2 * half ? Elem<T>::to_float(src[d < half ? d + half : d - half]) : 0.f;
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int d = d0 + i;
+                        if (valid && !is_v && d < 2 * half) {
+                            const float2 k = cs[d < half ? d : d - half];
+                            const float a = __fmul_rn(x[i], k.x), b = __fmul_rn(o[i], k.y);
+                            x[i] = d < half ? __fsub_rn(a, b) : __fadd_rn(a, b);
+                        }
+                    }
+                }
+                if (is_q) {
+                    if (valid) *reinterpret_cast<uint4 *>(reinterpret_cast<T *>(p.q_out) + ((int64_t)t * H + h) * D + d0) = narrow8<T>(x);
+                } else if constexpr (kCache == kCacheNone) {
+                    if (valid) *reinterpret_cast<uint4 *>(reinterpret_cast<T *>(p.k_out) + ((int64_t)t * Hk + h) * D + d0) = narrow8<T>(x);
+                }
+                if constexpr (kCache != kCacheNone) {
+                    if (__any_sync(0xffffffffu, valid && !is_q))  // a warp with queries alone has nothing to store
+                        store_row<T, D, kCache>(is_v ? p.v_cache : p.k_cache, x, slot, h, Hk, c, is_v ? p.v_scale : p.k_scale,
+                                                valid && !is_q && slot_ok);
+                }
+            }
+            w[0] = w2[0];
+            w[1] = w2[1];
         }
-        if constexpr (kCache != kCacheNone)
-            store_row<T, D, kCache>(is_v ? p.v_cache : p.k_cache, y, slot, h, Hk, c, is_v ? p.v_scale : p.k_scale,
-                                    valid && !is_q && slot_ok);
+        if (!more) return;
+        if (slot < 0 && slot2 >= 0) {  // nothing was in flight behind a padding token
+            w[0] = load(t2, first + mine);
+            w[1] = load(t2, first + mine + kRows);
+        }
+        t = t2;
+        slot = slot2;
+        buf ^= 1;
     }
 }
 
-// Cached rows back as 16-bit rows: D / 8 lanes per row, rows (token, K or V,
-// head) in the order they are written.
+// Cached rows back as 16-bit rows.  CTA = `tokens` tokens from blockIdx.x *
+// tokens on; a lane takes 16 elements of a (token, K or V, head) row, four rows
+// in flight.
 template <typename T, int D, int kCache>
-__global__ void __launch_bounds__(kThreads) gather_kernel(const GatherParams p) {
-    constexpr int LPR = D / 8;
+__global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherParams p, const int tokens) {
+    constexpr int LPR = D / 16;
+    constexpr int kInFlight = 4;
+    constexpr int kWords = kCache == kCache16 ? 8 : kCache == kCacheE4m3 ? 4 : 2;  // of a lane's 16 elements
+    const int Hk = p.num_kv_heads, t0 = (int)blockIdx.x * tokens;
+    const int items = min(tokens, p.num_tokens - t0) * 2 * Hk * LPR;
     pdl_wait();
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int c = (int)(i % LPR);
-    const int64_t row = i / LPR;
-    const int Hk = p.num_kv_heads;
-    const int64_t t = row / (2 * Hk);
-    if (t >= p.num_tokens) return;
-    const int rr = (int)(row % (2 * Hk)), h = rr % Hk;
-    const bool is_v = rr >= Hk;
-    const int64_t slot = p.slots[t];
-    if (slot < 0) return;
-    if (slot >= p.num_slots) {
-        if (rr == 0 && c == 0) flag_error(PA_DEVERR_SLOT);
-        return;
-    }
-    const void *cache = is_v ? p.v_cache : p.k_cache;
-    const float scale = is_v ? p.v_scale : p.k_scale;
-    const int64_t chunk = (slot / kBlock) * Hk + h;
-    const int off = (int)(slot % kBlock);
-    uint4 *dst = reinterpret_cast<uint4 *>(is_v ? p.value : p.key) + (t * Hk + h) * LPR + c;
-    if constexpr (kCache == kCache16) {
-        *dst = reinterpret_cast<const uint4 *>(cache)[(chunk * kBlock + off) * LPR + c];
-    } else {
-        float x[8];
-        if constexpr (kCache == kCacheE4m3) {
-            const uint2 w = reinterpret_cast<const uint2 *>(cache)[(chunk * kBlock + off) * LPR + c];
-            const uint32_t u[2] = {w.x, w.y};
+    for (int i0 = threadIdx.x; i0 < items; i0 += kInFlight * kGatherThreads) {
+        uint32_t w[kInFlight][kWords], ends[kInFlight];
+        int64_t dst[kInFlight];  // of the lane's 16 elements, in 16-byte words; -1: nothing
+        bool value[kInFlight];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float2 a = e4m3x2_to_float2((uint16_t)(u[k] & 0xffffu)), b = e4m3x2_to_float2((uint16_t)(u[k] >> 16));
-                x[4 * k] = a.x;
-                x[4 * k + 1] = a.y;
-                x[4 * k + 2] = b.x;
-                x[4 * k + 3] = b.y;
+        for (int u = 0; u < kInFlight; ++u) {
+            const int i = i0 + u * kGatherThreads;
+            dst[u] = -1;
+            if (i >= items) continue;
+            const int c = i % LPR, row = i / LPR, tok = row / (2 * Hk), rr = row - tok * 2 * Hk;
+            const int64_t t = t0 + tok, slot = p.slots[t];
+            if (slot < 0) continue;
+            if (slot >= p.num_slots) {
+                if (rr == 0 && c == 0) flag_error(PA_DEVERR_SLOT);
+                continue;
             }
-        } else {
-            const unsigned char *base = reinterpret_cast<const unsigned char *>(cache) + chunk * int4_chunk_bytes(D);
-            const uint32_t w = *reinterpret_cast<const uint32_t *>(base + off * (D / 2) + c * 4);
-            const float2 e = int4_ends(*reinterpret_cast<const uint32_t *>(base + int4_ends_offset(D) + off * 4));
+            value[u] = rr >= Hk;
+            const int h = value[u] ? rr - Hk : rr;
+            dst[u] = ((t * Hk + h) * LPR + c) * 2;
+            const unsigned char *cache = reinterpret_cast<const unsigned char *>(value[u] ? p.v_cache : p.k_cache);
+            const int64_t chunk = slot / kBlock * Hk + h;
+            const int off = (int)(slot % kBlock);
+            if constexpr (kCache == kCacheInt4) {
+                const unsigned char *base = cache + chunk * int4_chunk_bytes(D);
+                const uint2 v = *reinterpret_cast<const uint2 *>(base + off * (D / 2) + c * 8);
+                w[u][0] = v.x, w[u][1] = v.y;
+                ends[u] = *reinterpret_cast<const uint32_t *>(base + int4_ends_offset(D) + off * 4);
+            } else {
+                const uint4 *src = reinterpret_cast<const uint4 *>(cache) + ((chunk * kBlock + off) * LPR + c) * (kWords / 4);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = fmaf((float)((w >> (4 * k)) & 15u), e.x, e.y);  // the product is exact
+                for (int k = 0; k < kWords / 4; ++k) {
+                    const uint4 v = src[k];
+                    w[u][4 * k] = v.x, w[u][4 * k + 1] = v.y, w[u][4 * k + 2] = v.z, w[u][4 * k + 3] = v.w;
+                }
+            }
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] *= scale;
-        *dst = narrow8<T>(x);
+        for (int u = 0; u < kInFlight; ++u) {
+            if (dst[u] < 0) continue;
+            uint4 *out = reinterpret_cast<uint4 *>(value[u] ? p.value : p.key) + dst[u];
+            if constexpr (kCache == kCache16) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) out[k] = make_uint4(w[u][4 * k], w[u][4 * k + 1], w[u][4 * k + 2], w[u][4 * k + 3]);
+            } else {
+                const float scale = value[u] ? p.v_scale : p.k_scale;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float x[8];
+                    if constexpr (kCache == kCacheE4m3) {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const uint32_t v = w[u][2 * k + j];
+                            const float2 a = e4m3x2_to_float2((uint16_t)(v & 0xffffu)), b = e4m3x2_to_float2((uint16_t)(v >> 16));
+                            x[4 * j] = a.x, x[4 * j + 1] = a.y, x[4 * j + 2] = b.x, x[4 * j + 3] = b.y;
+                        }
+                    } else {
+                        const float2 e = int4_ends(ends[u]);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) x[j] = fmaf((float)((w[u][k] >> (4 * j)) & 15u), e.x, e.y);  // the product is exact
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] *= scale;
+                    out[k] = narrow8<T>(x);
+                }
+            }
+        }
+    }
+}
+
+template <typename T, int D, int kCache>
+cudaError_t launch_rope_c(const RopeParams &p, cudaStream_t stream) {
+    constexpr int kRows = 2 * (kThreads / (D / 8));
+    const int total = p.num_heads + (kCache == kCacheNone ? 1 : 2) * p.num_kv_heads;
+    // few tokens: a CTA per pass over a token's rows, to reach more SMs (each
+    // computes the sines again); many: a resident wave that walks over them
+    const int passes = (total + kRows - 1) / kRows;
+    const bool few = (int64_t)p.num_tokens * passes <= 1024;
+    const dim3 grid(few || p.num_tokens < kWave ? p.num_tokens : kWave, few ? passes : 1), block(kThreads);
+    const int pairs = p.half == 0 ? kPairsNone : p.interleaved ? kPairsInterleaved : p.half % 8 == 0 ? kPairsHalf : kPairsHalfOdd;
+    switch (pairs) {
+        case kPairsNone:
+            if constexpr (kCache == kCacheInt4) return launch_pdl(rope_kernel<T, D, kCache, kPairsNone>, grid, block, 0, stream, p);
+            return cudaErrorInvalidValue;  // only the 4-bit write comes without a rotation
+        case kPairsHalf: return launch_pdl(rope_kernel<T, D, kCache, kPairsHalf>, grid, block, 0, stream, p);
+        case kPairsInterleaved: return launch_pdl(rope_kernel<T, D, kCache, kPairsInterleaved>, grid, block, 0, stream, p);
+        default: return launch_pdl(rope_kernel<T, D, kCache, kPairsHalfOdd>, grid, block, 0, stream, p);
     }
 }
 
 template <typename T, int D>
 cudaError_t launch_rope_d(const RopeParams &p, int cache, cudaStream_t stream) {
-    const dim3 grid(p.num_tokens), block(kThreads);
     switch (cache) {
-        case kCacheNone: return launch_pdl(rope_kernel<T, D, kCacheNone>, grid, block, 0, stream, p);
-        case kCache16: return launch_pdl(rope_kernel<T, D, kCache16>, grid, block, 0, stream, p);
-        case kCacheE4m3: return launch_pdl(rope_kernel<T, D, kCacheE4m3>, grid, block, 0, stream, p);
-        default: return launch_pdl(rope_kernel<T, D, kCacheInt4>, grid, block, 0, stream, p);
+        case kCacheNone: return launch_rope_c<T, D, kCacheNone>(p, stream);
+        case kCache16: return launch_rope_c<T, D, kCache16>(p, stream);
+        case kCacheE4m3: return launch_rope_c<T, D, kCacheE4m3>(p, stream);
+        default: return launch_rope_c<T, D, kCacheInt4>(p, stream);
     }
 }
 
 template <typename T, int D>
 cudaError_t launch_gather_d(const GatherParams &p, int cache, cudaStream_t stream) {
-    const int64_t items = (int64_t)p.num_tokens * 2 * p.num_kv_heads * (D / 8);
-    const dim3 grid((unsigned)((items + kThreads - 1) / kThreads)), block(kThreads);
+    // as many tokens per CTA as give its lanes their four rows each
+    const int per_token = 2 * p.num_kv_heads * (D / 16);
+    const int tokens = per_token >= 4 * kGatherThreads ? 1 : 4 * kGatherThreads / per_token;
+    const dim3 grid((p.num_tokens - 1) / tokens + 1), block(kGatherThreads);
     switch (cache) {
-        case kCache16: return launch_pdl(gather_kernel<T, D, kCache16>, grid, block, 0, stream, p);
-        case kCacheE4m3: return launch_pdl(gather_kernel<T, D, kCacheE4m3>, grid, block, 0, stream, p);
-        default: return launch_pdl(gather_kernel<T, D, kCacheInt4>, grid, block, 0, stream, p);
+        case kCache16: return launch_pdl(gather_kernel<T, D, kCache16>, grid, block, 0, stream, p, tokens);
+        case kCacheE4m3: return launch_pdl(gather_kernel<T, D, kCacheE4m3>, grid, block, 0, stream, p, tokens);
+        default: return launch_pdl(gather_kernel<T, D, kCacheInt4>, grid, block, 0, stream, p, tokens);
     }
 }
 
