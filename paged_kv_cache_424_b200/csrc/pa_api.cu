@@ -546,6 +546,8 @@ pa_status pa_reshape_and_cache_int4(const void *key, const void *value, void *k_
     if (!key || !value || !k_cache || !v_cache || !slot_mapping) return fail(PA_ERR_NULL, "a required pointer is NULL");
     if (!aligned16(key) || !aligned16(value) || !aligned16(k_cache) || !aligned16(v_cache))
         return fail(PA_ERR_ALIGN, "key, value and caches must be 16-byte aligned");
+    if ((int64_t)num_tokens * 2 * dims->num_kv_heads > (int64_t)1 << 30)
+        return fail(PA_ERR_SHAPE, "num_tokens * num_kv_heads must be <= 2^29");
     pa::RopeParams p{};
     p.k = key;
     p.v = value;
@@ -576,6 +578,8 @@ pa_status pa_gather_cache(void *key, void *value, const void *k_cache, const voi
     if (!key || !value || !k_cache || !v_cache || !slot_mapping) return fail(PA_ERR_NULL, "a required pointer is NULL");
     if (!aligned16(key) || !aligned16(value) || !aligned16(k_cache) || !aligned16(v_cache))
         return fail(PA_ERR_ALIGN, "key, value and caches must be 16-byte aligned");
+    if ((int64_t)num_tokens * 2 * dims->num_kv_heads * (dims->head_dim / 16) > (int64_t)1 << 30)
+        return fail(PA_ERR_SHAPE, "num_tokens * num_kv_heads * head_dim must be <= 2^33");
     pa::GatherParams p{};
     p.key = key;
     p.value = value;

@@ -9,9 +9,12 @@
 // CTA = one token (or some of its rows, when there are few tokens).  Its first
 // rotary_dim / 2 threads compute the token's (m cos, m sin) pairs in fp64 and
 // share them through shared memory, so the sines are computed once per token
-// and not once per head.  Then D / 8 lanes take a row (a head's D elements): 16
-// bytes per lane, the partner elements of a pair by a shuffle, the next pass's
-// rows in flight while one is worked on.
+// and not once per head.  Then D / 16 lanes take a row (a head's D elements): a
+// lane has two pieces of 8 elements that hold both ends of its pairs, so that
+// nothing is exchanged and each sine serves both; the next pass's rows are in
+// flight while one is worked on.
+#include <algorithm>
+
 #include "pa_common.cuh"
 #include "pa_decode.h"
 #include "pa_int4.cuh"
@@ -103,6 +106,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
@@ -184,30 +192,38 @@ __device__ __forceinline__ uint2 e4m3_codes(const float (&x)[8], float scale) {
     return make_uint2(u[0], u[1]);
 }
 
-// The row of `slot` and KV head h takes the 8 elements x (dims 8 c ..) of
-// each of the row's LPR lanes (all of them converged; `live`: this lane's
-// row is written).
+// The row of `slot` and KV head h takes this lane's pieces xa (dims 8 ca ..) and
+// xb (8 cb ..); all of the row's D / 16 lanes converged, `live`: the row is
+// written.
 template <typename T, int D, int kCache>
-__device__ __forceinline__ void store_row(void *cache, const float (&x)[8], int64_t slot, int h, int num_kv_heads,
-                                          int c, float scale, bool live) {
-    constexpr int LPR = D / 8;
+__device__ __forceinline__ void store_row(void *cache, const float (&xa)[8], const float (&xb)[8], int64_t slot, int h,
+                                          int num_kv_heads, int ca, int cb, float scale, bool live) {
+    constexpr int kPieces = D / 8;
     const int64_t blk = slot / kBlock;
     const int off = (int)(slot % kBlock);
     const int64_t chunk = blk * num_kv_heads + h;
     if constexpr (kCache == kCache16) {
-        if (live) reinterpret_cast<uint4 *>(cache)[(chunk * kBlock + off) * LPR + c] = narrow8<T>(x);
+        if (live) {
+            uint4 *dst = reinterpret_cast<uint4 *>(cache) + (chunk * kBlock + off) * kPieces;
+            dst[ca] = narrow8<T>(xa);
+            dst[cb] = narrow8<T>(xb);
+        }
     } else if constexpr (kCache == kCacheE4m3) {
-        if (live) reinterpret_cast<uint2 *>(cache)[(chunk * kBlock + off) * LPR + c] = e4m3_codes(x, scale);
+        if (live) {
+            uint2 *dst = reinterpret_cast<uint2 *>(cache) + (chunk * kBlock + off) * kPieces;
+            dst[ca] = e4m3_codes(xa, scale);
+            dst[cb] = e4m3_codes(xb, scale);
+        }
     } else if constexpr (kCache == kCacheInt4) {
         // a NaN goes through both; an infinity makes the range infinite or NaN
-        float lo = x[0], hi = x[0];
+        float lo = min_nan(xa[0], xb[0]), hi = max_nan(xa[0], xb[0]);
 #pragma unroll
         for (int i = 1; i < 8; ++i) {
-            lo = min_nan(lo, x[i]);
-            hi = max_nan(hi, x[i]);
+            lo = min_nan(lo, min_nan(xa[i], xb[i]));
+            hi = max_nan(hi, max_nan(xa[i], xb[i]));
         }
 #pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) {
+        for (int o = D / 32; o > 0; o >>= 1) {
             lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
             hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
         }
@@ -216,204 +232,256 @@ __device__ __forceinline__ void store_row(void *cache, const float (&x)[8], int6
         const float low = __bfloat162float(lb);
         __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(__fsub_rn(hi, low), 15.f));
         const float sc = __bfloat162float(sb);
-        uint32_t codes = 0;
-        if (!(fabsf(sc) < INFINITY))  // a NaN or an infinity in the row, or a range past fp32's
+        uint32_t code_a = 0, code_b = 0;
+        if (!(fabsf(sc) < INFINITY)) {  // a NaN or an infinity in the row, or a range past fp32's
             lb = sb = __float2bfloat16_rn(NAN);
-        else if (sc != 0.f)
-            codes = int4_codes(x, low, sc);
+        } else if (sc != 0.f) {
+            code_a = int4_codes(xa, low, sc);
+            code_b = int4_codes(xb, low, sc);
+        }
         unsigned char *base = reinterpret_cast<unsigned char *>(cache) + chunk * int4_chunk_bytes(D);
-        *reinterpret_cast<uint32_t *>(base + off * (D / 2) + c * 4) = codes;
-        if (c == 0) {
+        uint32_t *row = reinterpret_cast<uint32_t *>(base + off * (D / 2));
+        if (cb == ca + 1) {
+            *reinterpret_cast<uint2 *>(row + ca) = make_uint2(code_a, code_b);
+        } else {
+            row[ca] = code_a;
+            row[cb] = code_b;
+        }
+        if (ca == 0) {
             const uint32_t ends = (uint32_t)__bfloat16_as_ushort(sb) | ((uint32_t)__bfloat16_as_ushort(lb) << 16);
             *reinterpret_cast<uint32_t *>(base + int4_ends_offset(D) + off * 4) = ends;
         }
     }
 }
 
-constexpr int kWave = 148 * 7;  // CTAs that a device holds at once
+constexpr int kWave = 148 * 8;  // CTAs that a device holds at once
 
 // How a row's pairs lie in its lanes' 8 dims.
-enum { kPairsNone = 0, kPairsHalf = 1, kPairsInterleaved = 2, kPairsHalfOdd = 3 };  // kPairsHalf: rotary_dim / 2 a multiple of 8
+enum { kPairsHalf = 0, kPairsInterleaved = 1, kPairsHalfOdd = 2 };  // kPairsHalf: rotary_dim / 2 a multiple of 8
 
 // CTA = tokens blockIdx.x, blockIdx.x + gridDim.x, ...; of each the passes
-// blockIdx.y, blockIdx.y + gridDim.y, ... over its rows, 2 kRows rows each.
+// blockIdx.y, blockIdx.y + gridDim.y, ... over its rows, kRows rows each.
 template <typename T, int D, int kCache, int kPairs>
-__global__ void __launch_bounds__(kThreads, 7) rope_kernel(const RopeParams p) {
-    constexpr int LPR = D / 8;             // lanes per row
-    constexpr int kRows = kThreads / LPR;  // rows that the CTA's lanes hold at once
-    __shared__ __align__(16) float2 cs_s[2][kMaxHalf];
+__global__ void __launch_bounds__(kThreads, 8) rope_kernel(const RopeParams p) {
+    constexpr int LPR = D / 16;            // lanes per row
+    constexpr int kRows = kThreads / LPR;  // rows of a pass
+    __shared__ __align__(16) float cos_s[2][kMaxHalf], sin_s[2][kMaxHalf];
     const int tid = threadIdx.x, lane = tid & 31;
     // The decode kernels read q before they wait for the kernel in front of
     // them, so a kernel that writes q or k does not let the next one start
     // early; a cache write alone does.
     if (!p.q_out && !p.k_out) pdl_launch_dependents();
     const int half = p.half;
-    const int c = lane % LPR, d0 = 8 * c;  // this lane's dims d0 .. d0 + 7
+    // this lane's pieces ca and cb of 8 dims: half: piece j and the one half / 8
+    // behind it, which hold both ends of pairs 8 j .. 8 j + 7 (j < half / 8; the
+    // dims past rotary_dim two by two); otherwise neighbours, which interleaved
+    // hold the same pairs
+    const int j = lane % LPR;
+    const int q8 = kPairs == kPairsHalf ? half / 8 : 0;
+    const int ca = kPairs != kPairsHalf ? 2 * j : j < q8 ? j : 2 * q8 + 2 * (j - q8);
+    const int cb = kPairs != kPairsHalf ? 2 * j + 1 : j < q8 ? j + q8 : ca + 1;
     const int H = p.num_heads, Hk = p.num_kv_heads;
     const int total = H + (kCache == kCacheNone ? Hk : 2 * Hk);
-    const int first = (int)blockIdx.y * 2 * kRows, step = 2 * kRows * (int)gridDim.y;  // of the CTA's passes
-    const int mine = tid / LPR;                                                        // this lane's row in a pass
+    const int first = (int)blockIdx.y * kRows, step = kRows * (int)gridDim.y;  // of the CTA's passes
+    const int mine = tid / LPR;                                                // this lane's row in a pass
     // positions, slots and frequencies are no kernel of this library's output:
     // the first token's sines are computed before the wait for the kernel in
     // front, a later one's while the token before it is worked on
-    const double freq = kPairs != kPairsNone && tid < half ? p.inv_freq[tid] * 0.15915494309189533576888 : 0.0;
+    const double freq = tid < half ? p.inv_freq[tid] * 0.15915494309189533576888 : 0.0;
     auto sines = [&](int t, int buf) {
-        if constexpr (kPairs != kPairsNone) {
-            if (tid < half) {
-                double s, co;
-                sincos_turns((double)p.positions[t] * freq, &s, &co);
-                if (p.inverse) s = -s;
-                cs_s[buf][tid] = make_float2((float)(co * p.magnitude), (float)(s * p.magnitude));
-            }
-        }
+        if (tid >= half) return;
+        double s, co;
+        sincos_turns((double)p.positions[t] * freq, &s, &co);
+        if (p.inverse) s = -s;
+        cos_s[buf][tid] = (float)(co * p.magnitude);
+        sin_s[buf][tid] = (float)(s * p.magnitude);
     };
     auto slot_of = [&](int t) -> int64_t { return kCache == kCacheNone ? 0 : p.slots[t]; };
-    auto load = [&](int t, int row) -> uint4 {  // queries, keys, values in this order
-        if (row >= total) return make_uint4(0, 0, 0, 0);
+    auto load = [&](int t, int row, uint4 (&w)[2]) {  // queries, keys, values in this order
+        w[0] = w[1] = make_uint4(0, 0, 0, 0);
+        if (row >= total) return;
         const T *base = row < H ? reinterpret_cast<const T *>(p.q)
                         : row < H + Hk ? reinterpret_cast<const T *>(p.k) : reinterpret_cast<const T *>(p.v);
         const int64_t stride = row < H ? p.q_stride : row < H + Hk ? p.k_stride : p.v_stride;
         const int h = row < H ? row : row < H + Hk ? row - H : row - H - Hk;
-        return *reinterpret_cast<const uint4 *>(base + t * stride + (h * D + d0));
+        const uint4 *src = reinterpret_cast<const uint4 *>(base + t * stride) + h * (D / 8);
+        w[0] = src[ca];
+        w[1] = src[cb];
     };
     int t = blockIdx.x, buf = 0;
     int64_t slot = slot_of(t);
     if (slot >= 0) sines(t, 0);
     pdl_wait();
     uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (slot >= 0) {
-        w[0] = load(t, first + mine);
-        w[1] = load(t, first + mine + kRows);
-    }
+    if (slot >= 0) load(t, first + mine, w);
     for (;;) {
         const int t2 = t + (int)gridDim.x;
         const bool more = t2 < p.num_tokens;
         const int64_t slot2 = more ? slot_of(t2) : -1;
-        if constexpr (kPairs != kPairsNone) __syncthreads();  // this token's sines are there, those of the one before are done with
+        __syncthreads();  // this token's sines are there, those of the one before are done with
         if (more && slot2 >= 0) sines(t2, buf ^ 1);
         const bool slot_ok = kCache == kCacheNone || slot < p.num_slots;
         if (!slot_ok && tid == 0 && blockIdx.y == 0) flag_error(PA_DEVERR_SLOT);
-        const float2 *cs = cs_s[buf];
         // a token with a negative slot is padding: nothing of it is read or written
         // (the loop's bounds are the CTA's: every lane of a warp stays in it)
         for (int pass = slot < 0 ? total : first; pass < total; pass += step) {
-            const int row0 = pass + mine;
-            uint4 w2[2];  // the next pass's rows, or the next token's
-            const bool last = pass + step >= total;
+            const int row = pass + mine;
+            uint4 w2[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};  // the next pass's row, or the next token's
+            if (pass + step < total)
+                load(t, row + step, w2);
+            else if (slot2 >= 0)
+                load(t2, first + mine, w2);
+            const bool valid = row < total, is_q = row < H, is_v = row >= H + Hk;
+            const int h = is_q ? row : is_v ? row - H - Hk : row - H;
+            float xa[8], xb[8];
+            widen8<T>(w[0], xa);
+            widen8<T>(w[1], xb);
+            if constexpr (kPairs == kPairsHalf) {
+                if (!is_v && j < q8) {
+                    // a' = a cos - b sin, b' = b cos + a sin
+                    const float4 *co = reinterpret_cast<const float4 *>(cos_s[buf] + 8 * j);
+                    const float4 *si = reinterpret_cast<const float4 *>(sin_s[buf] + 8 * j);
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-                w2[u] = !last ? load(t, row0 + step + u * kRows)
-                        : slot2 >= 0 ? load(t2, first + mine + u * kRows) : make_uint4(0, 0, 0, 0);
+                    for (int k = 0; k < 2; ++k) {
+                        const float4 f = co[k], g = si[k];
+                        const uint64_t c2[2] = {pk2(f.x, f.y), pk2(f.z, f.w)}, s2[2] = {pk2(g.x, g.y), pk2(g.z, g.w)};
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int row = row0 + u * kRows;
-                const bool valid = row < total, is_q = row < H, is_v = row >= H + Hk;
-                const int h = is_q ? row : is_v ? row - H - Hk : row - H;
-                float x[8];
-                widen8<T>(w[u], x);
-                if constexpr (kPairs == kPairsInterleaved) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (valid && !is_v && 4 * c + i < half) {
-                            const float2 k = cs[4 * c + i];
-                            const float a = x[2 * i], b = x[2 * i + 1];
-                            x[2 * i] = __fsub_rn(__fmul_rn(a, k.x), __fmul_rn(b, k.y));
-                            x[2 * i + 1] = __fadd_rn(__fmul_rn(b, k.x), __fmul_rn(a, k.y));
+                        for (int i = 0; i < 2; ++i) {
+                            const int e = 4 * k + 2 * i;
+                            const uint64_t a = pk2(xa[e], xa[e + 1]), b = pk2(xb[e], xb[e + 1]);
+                            const float2 ya = up2(sub2(mul2(a, c2[i]), mul2(b, s2[i])));
+                            const float2 yb = up2(add2(mul2(b, c2[i]), mul2(a, s2[i])));
+                            xa[e] = ya.x, xa[e + 1] = ya.y;
+                            xb[e] = yb.x, xb[e + 1] = yb.y;
                         }
                     }
-                } else if constexpr (kPairs == kPairsHalf) {
-                    const int q8 = half / 8;  // lanes of a half
-                    const int other = lane - c + (c < q8 ? c + q8 : c < 2 * q8 ? c - q8 : c);
-                    uint4 wo;
-                    wo.x = __shfl_sync(0xffffffffu, w[u].x, other);
-                    wo.y = __shfl_sync(0xffffffffu, w[u].y, other);
-                    wo.z = __shfl_sync(0xffffffffu, w[u].z, other);
-                    wo.w = __shfl_sync(0xffffffffu, w[u].w, other);
-                    if (valid && !is_v && c < 2 * q8) {
-                        // a' = a cos + (-b) sin, b' = b cos + a sin
-                        const uint32_t sign = c < q8 ? 0x80008000u : 0u;
-                        wo = make_uint4(wo.x ^ sign, wo.y ^ sign, wo.z ^ sign, wo.w ^ sign);
-                        float o[8];
-                        widen8<T>(wo, o);
-                        const float4 *k = reinterpret_cast<const float4 *>(cs + (c < q8 ? d0 : d0 - half));
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float4 f = k[i];  // (cos, sin) of two pairs
-                            const float2 y = up2(add2(mul2(pk2(x[2 * i], x[2 * i + 1]), pk2(f.x, f.z)),
-                                                      mul2(pk2(o[2 * i], o[2 * i + 1]), pk2(f.y, f.w))));
-                            x[2 * i] = y.x;
-                            x[2 * i + 1] = y.y;
-                        }
-                    }
-                } else if constexpr (kPairs == kPairsHalfOdd) {
-                    // pairs that straddle the lanes' 8 dims: single elements, all
-                    // read before the row is written (it may be written in place)
-                    float o[8];
-                    const T *src = is_q ? reinterpret_cast<const T *>(p.q) + t * p.q_stride + h * D
-                                        : reinterpret_cast<const T *>(p.k) + t * p.k_stride + h * D;
+                }
+            } else if constexpr (kPairs == kPairsInterleaved) {
+                if (!is_v) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const int d = d0 + i;
-                        o[i] = valid && !is_v && d < 2 * half ? Elem<T>::to_float(src[d < half ? d + half : d - half]) : 0.f;
-                    }
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int d = d0 + i;
-                        if (valid && !is_v && d < 2 * half) {
-                            const float2 k = cs[d < half ? d : d - half];
-                            const float a = __fmul_rn(x[i], k.x), b = __fmul_rn(o[i], k.y);
-                            x[i] = d < half ? __fsub_rn(a, b) : __fadd_rn(a, b);
+                        float *x = i < 4 ? xa + 2 * i : xb + 2 * i - 8;
+                        const int pair = 8 * j + i;
+                        if (pair < half) {
+                            const float co = cos_s[buf][pair], si = sin_s[buf][pair], a = x[0], b = x[1];
+                            x[0] = __fsub_rn(__fmul_rn(a, co), __fmul_rn(b, si));
+                            x[1] = __fadd_rn(__fmul_rn(b, co), __fmul_rn(a, si));
                         }
                     }
                 }
-                if (is_q) {
-                    if (valid) *reinterpret_cast<uint4 *>(reinterpret_cast<T *>(p.q_out) + ((int64_t)t * H + h) * D + d0) = narrow8<T>(x);
-                } else if constexpr (kCache == kCacheNone) {
-                    if (valid) *reinterpret_cast<uint4 *>(reinterpret_cast<T *>(p.k_out) + ((int64_t)t * Hk + h) * D + d0) = narrow8<T>(x);
+            } else if constexpr (kPairs == kPairsHalfOdd) {
+                // pairs that straddle the pieces: single elements, all read before
+                // the row is written (it may be written in place)
+                const T *src = is_q ? reinterpret_cast<const T *>(p.q) + t * p.q_stride + h * D
+                                    : reinterpret_cast<const T *>(p.k) + t * p.k_stride + h * D;
+                float o[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int d = 16 * j + i;
+                    o[i] = valid && !is_v && d < 2 * half ? Elem<T>::to_float(src[d < half ? d + half : d - half]) : 0.f;
                 }
-                if constexpr (kCache != kCacheNone) {
-                    if (__any_sync(0xffffffffu, valid && !is_q))  // a warp with queries alone has nothing to store
-                        store_row<T, D, kCache>(is_v ? p.v_cache : p.k_cache, x, slot, h, Hk, c, is_v ? p.v_scale : p.k_scale,
-                                                valid && !is_q && slot_ok);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int d = 16 * j + i;
+                    float &x = i < 8 ? xa[i] : xb[i - 8];
+                    if (!is_v && d < 2 * half) {
+                        const int pair = d < half ? d : d - half;
+                        const float a = __fmul_rn(x, cos_s[buf][pair]), b = __fmul_rn(o[i], sin_s[buf][pair]);
+                        x = d < half ? __fsub_rn(a, b) : __fadd_rn(a, b);
+                    }
                 }
+            }
+            if (is_q || kCache == kCacheNone) {
+                if (valid) {
+                    uint4 *dst = is_q ? reinterpret_cast<uint4 *>(p.q_out) + ((int64_t)t * H + h) * (D / 8)
+                                      : reinterpret_cast<uint4 *>(p.k_out) + ((int64_t)t * Hk + h) * (D / 8);
+                    dst[ca] = narrow8<T>(xa);
+                    dst[cb] = narrow8<T>(xb);
+                }
+            }
+            if constexpr (kCache != kCacheNone) {
+                if (__any_sync(0xffffffffu, valid && !is_q))  // a warp with queries alone has nothing to store
+                    store_row<T, D, kCache>(is_v ? p.v_cache : p.k_cache, xa, xb, slot, h, Hk, ca, cb,
+                                            is_v ? p.v_scale : p.k_scale, valid && !is_q && slot_ok);
             }
             w[0] = w2[0];
             w[1] = w2[1];
         }
         if (!more) return;
-        if (slot < 0 && slot2 >= 0) {  // nothing was in flight behind a padding token
-            w[0] = load(t2, first + mine);
-            w[1] = load(t2, first + mine + kRows);
-        }
+        if (slot < 0 && slot2 >= 0) load(t2, first + mine, w);  // nothing was in flight behind a padding token
         t = t2;
         slot = slot2;
         buf ^= 1;
     }
 }
 
-// Cached rows back as 16-bit rows.  CTA = `tokens` tokens from blockIdx.x *
-// tokens on; a lane takes 16 elements of a (token, K or V, head) row, four rows
-// in flight.
+// The 4-bit cache write without a rotation: D / 16 lanes per (token, K or V,
+// head) row, the rows of the whole call dealt out to the grid's lane groups, the
+// next row in flight.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) write_int4_kernel(const RopeParams p) {
+    constexpr int LPR = D / 16;
+    pdl_launch_dependents();
+    const int j = threadIdx.x % LPR, Hk = p.num_kv_heads, rows = p.num_tokens * 2 * Hk;
+    const int groups = (int)gridDim.x * (kThreads / LPR);
+    // lanes of a warp stay together: its first row decides the loop
+    int base = (int)blockIdx.x * (kThreads / LPR) + threadIdx.x / 32 * (32 / LPR);
+    const int mine = threadIdx.x % 32 / LPR;
+    auto slot_of = [&](int row) -> int64_t { return row < rows ? p.slots[row / (2 * Hk)] : -1; };
+    auto load = [&](int row, int64_t slot, uint4 (&w)[2]) {
+        w[0] = w[1] = make_uint4(0, 0, 0, 0);
+        if (slot < 0 || slot >= p.num_slots) return;
+        const int t = row / (2 * Hk), rr = row - t * 2 * Hk;
+        const T *src = rr < Hk ? reinterpret_cast<const T *>(p.k) + t * p.k_stride + rr * D
+                               : reinterpret_cast<const T *>(p.v) + t * p.v_stride + (rr - Hk) * D;
+        w[0] = reinterpret_cast<const uint4 *>(src)[2 * j];
+        w[1] = reinterpret_cast<const uint4 *>(src)[2 * j + 1];
+    };
+    int64_t slot = slot_of(base + mine);
+    pdl_wait();
+    uint4 w[2];
+    load(base + mine, slot, w);
+    for (; base < rows; base += groups) {
+        const int row = base + mine, row2 = row + groups;
+        const int64_t slot2 = row2 < rows ? slot_of(row2) : -1;
+        uint4 w2[2];
+        load(row2, slot2, w2);
+        const int t = row / (2 * Hk), rr = row - t * 2 * Hk;
+        if (slot >= p.num_slots && rr == 0 && j == 0) flag_error(PA_DEVERR_SLOT);
+        float xa[8], xb[8];
+        widen8<T>(w[0], xa);
+        widen8<T>(w[1], xb);
+        store_row<T, D, kCacheInt4>(rr < Hk ? p.k_cache : p.v_cache, xa, xb, slot, rr < Hk ? rr : rr - Hk, Hk, 2 * j, 2 * j + 1,
+                                    1.f, slot >= 0 && slot < p.num_slots);
+        slot = slot2;
+        w[0] = w2[0];
+        w[1] = w2[1];
+    }
+}
+
+// Cached rows back as 16-bit rows: a lane takes 16 elements of a (token, K or
+// V, head) row, up to four such in flight, a grid's width apart.
 template <typename T, int D, int kCache>
-__global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherParams p, const int tokens) {
+__global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherParams p) {
     constexpr int LPR = D / 16;
     constexpr int kInFlight = 4;
     constexpr int kWords = kCache == kCache16 ? 8 : kCache == kCacheE4m3 ? 4 : 2;  // of a lane's 16 elements
-    const int Hk = p.num_kv_heads, t0 = (int)blockIdx.x * tokens;
-    const int items = min(tokens, p.num_tokens - t0) * 2 * Hk * LPR;
+    const int Hk = p.num_kv_heads, items = p.num_tokens * 2 * Hk * LPR, width = (int)gridDim.x * kGatherThreads;
     pdl_wait();
-    for (int i0 = threadIdx.x; i0 < items; i0 += kInFlight * kGatherThreads) {
+    {
+        const int i0 = (int)blockIdx.x * kGatherThreads + threadIdx.x;
         uint32_t w[kInFlight][kWords], ends[kInFlight];
         int64_t dst[kInFlight];  // of the lane's 16 elements, in 16-byte words; -1: nothing
         bool value[kInFlight];
 #pragma unroll
         for (int u = 0; u < kInFlight; ++u) {
-            const int i = i0 + u * kGatherThreads;
+            const int64_t at = i0 + (int64_t)u * width;
             dst[u] = -1;
-            if (i >= items) continue;
+            if (at >= items) continue;
+            const int i = (int)at;
             const int c = i % LPR, row = i / LPR, tok = row / (2 * Hk), rr = row - tok * 2 * Hk;
-            const int64_t t = t0 + tok, slot = p.slots[t];
+            const int64_t t = tok, slot = p.slots[t];
             if (slot < 0) continue;
             if (slot >= p.num_slots) {
                 if (rr == 0 && c == 0) flag_error(PA_DEVERR_SLOT);
@@ -474,18 +542,15 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const GatherPara
 
 template <typename T, int D, int kCache>
 cudaError_t launch_rope_c(const RopeParams &p, cudaStream_t stream) {
-    constexpr int kRows = 2 * (kThreads / (D / 8));
+    constexpr int kRows = kThreads / (D / 16);
     const int total = p.num_heads + (kCache == kCacheNone ? 1 : 2) * p.num_kv_heads;
     // few tokens: a CTA per pass over a token's rows, to reach more SMs (each
     // computes the sines again); many: a resident wave that walks over them
     const int passes = (total + kRows - 1) / kRows;
     const bool few = (int64_t)p.num_tokens * passes <= 1024;
     const dim3 grid(few || p.num_tokens < kWave ? p.num_tokens : kWave, few ? passes : 1), block(kThreads);
-    const int pairs = p.half == 0 ? kPairsNone : p.interleaved ? kPairsInterleaved : p.half % 8 == 0 ? kPairsHalf : kPairsHalfOdd;
+    const int pairs = p.interleaved ? kPairsInterleaved : p.half % 8 == 0 ? kPairsHalf : kPairsHalfOdd;
     switch (pairs) {
-        case kPairsNone:
-            if constexpr (kCache == kCacheInt4) return launch_pdl(rope_kernel<T, D, kCache, kPairsNone>, grid, block, 0, stream, p);
-            return cudaErrorInvalidValue;  // only the 4-bit write comes without a rotation
         case kPairsHalf: return launch_pdl(rope_kernel<T, D, kCache, kPairsHalf>, grid, block, 0, stream, p);
         case kPairsInterleaved: return launch_pdl(rope_kernel<T, D, kCache, kPairsInterleaved>, grid, block, 0, stream, p);
         default: return launch_pdl(rope_kernel<T, D, kCache, kPairsHalfOdd>, grid, block, 0, stream, p);
@@ -494,6 +559,11 @@ cudaError_t launch_rope_c(const RopeParams &p, cudaStream_t stream) {
 
 template <typename T, int D>
 cudaError_t launch_rope_d(const RopeParams &p, int cache, cudaStream_t stream) {
+    if (p.half == 0) {  // the 4-bit cache write
+        constexpr int kRows = kThreads / (D / 16);
+        const int64_t ctas = ((int64_t)p.num_tokens * 2 * p.num_kv_heads + kRows - 1) / kRows;
+        return launch_pdl(write_int4_kernel<T, D>, dim3((unsigned)std::min<int64_t>(ctas, 148 * 12)), dim3(kThreads), 0, stream, p);
+    }
     switch (cache) {
         case kCacheNone: return launch_rope_c<T, D, kCacheNone>(p, stream);
         case kCache16: return launch_rope_c<T, D, kCache16>(p, stream);
@@ -504,14 +574,14 @@ cudaError_t launch_rope_d(const RopeParams &p, int cache, cudaStream_t stream) {
 
 template <typename T, int D>
 cudaError_t launch_gather_d(const GatherParams &p, int cache, cudaStream_t stream) {
-    // as many tokens per CTA as give its lanes their four rows each
-    const int per_token = 2 * p.num_kv_heads * (D / 16);
-    const int tokens = per_token >= 4 * kGatherThreads ? 1 : 4 * kGatherThreads / per_token;
-    const dim3 grid((p.num_tokens - 1) / tokens + 1), block(kGatherThreads);
+    // one row per lane while that still fits the device's threads twice over, four beyond
+    const int64_t items = (int64_t)p.num_tokens * 2 * p.num_kv_heads * (D / 16);
+    const int64_t ctas = (items + kGatherThreads - 1) / kGatherThreads;
+    const dim3 grid((unsigned)std::max(std::min<int64_t>(ctas, 2 * 148 * 8), (ctas + 3) / 4)), block(kGatherThreads);
     switch (cache) {
-        case kCache16: return launch_pdl(gather_kernel<T, D, kCache16>, grid, block, 0, stream, p, tokens);
-        case kCacheE4m3: return launch_pdl(gather_kernel<T, D, kCacheE4m3>, grid, block, 0, stream, p, tokens);
-        default: return launch_pdl(gather_kernel<T, D, kCacheInt4>, grid, block, 0, stream, p, tokens);
+        case kCache16: return launch_pdl(gather_kernel<T, D, kCache16>, grid, block, 0, stream, p);
+        case kCacheE4m3: return launch_pdl(gather_kernel<T, D, kCacheE4m3>, grid, block, 0, stream, p);
+        default: return launch_pdl(gather_kernel<T, D, kCacheInt4>, grid, block, 0, stream, p);
     }
 }
 
