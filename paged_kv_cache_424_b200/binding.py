@@ -10,6 +10,7 @@ loads the library and raises :class:`LibraryMissing` if it is not built.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Sequence
 
@@ -161,15 +162,15 @@ def _dtype_code(t: torch.Tensor) -> int:
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _stream(stream) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
-        stream = stream.cuda_stream
-    return ctypes.c_void_p(int(stream))
+        return stream.cuda_stream
+    return int(stream)
 
 
 def _check(status: int) -> None:
@@ -191,6 +192,28 @@ def int4_cache_shape(num_blocks: int, num_kv_heads: int, head_dim: int) -> tuple
 
 def _is_int4(cache: torch.Tensor) -> bool:
     return cache.dim() == 3 and cache.dtype == torch.uint8
+
+
+def _on_device(first: torch.Tensor, *others: Optional[torch.Tensor]) -> None:
+    """All on one CUDA device, the current one (whose streams the calls use)."""
+    dev = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            dev = -1
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError("tensors must be on the current CUDA device")
+
+
+def _dense(*ts: Optional[torch.Tensor]) -> None:
+    for t in ts:
+        if t is not None and not t.is_contiguous():
+            raise ValueError("outputs, caches and index tensors must be contiguous")
+
+
+@functools.lru_cache(maxsize=512)
+def _dims_ref(*fields: int):
+    """A pa_dims by reference; the calls only read it."""
+    return ctypes.byref(pa_dims(*fields))
 
 
 def _kv_code(cache: torch.Tensor) -> int:
@@ -321,17 +344,26 @@ def pa_decode_int4(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_
                    stream=None) -> torch.Tensor:
     """pa_decode over 4-bit caches (uint8 tensors of int4_cache_shape): an
     element is code * scale + low of its row."""
-    _need_cuda(out, q, k_cache, v_cache, block_tables, context_lens, workspace)
-    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
-        raise TypeError("block_tables and context_lens must be int32")
     if not _is_int4(k_cache) or not _is_int4(v_cache):
         raise TypeError("4-bit caches must be uint8 tensors of int4_cache_shape")
-    dims = dims_of(q, k_cache, block_tables)
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise TypeError("block_tables and context_lens must be int32")
+    S, H, D = q.shape
+    NB, Hk, nbytes = k_cache.shape
+    if nbytes != 8 * D + 64:
+        raise ValueError("q and k_cache disagree on head_dim")
+    if out.shape != q.shape or out.dtype != q.dtype or v_cache.shape != k_cache.shape or block_tables.dim() != 2 or \
+            block_tables.shape[0] != S or context_lens.numel() != S:
+        raise ValueError("out must be as q, v_cache as k_cache, block_tables [num_seqs, blocks], context_lens [num_seqs]")
+    _on_device(q, out, k_cache, v_cache, block_tables, context_lens, workspace)
+    _dense(out, q, k_cache, v_cache, block_tables, context_lens, workspace)
+    dims = _dims_ref(S, H, Hk, D, 16, block_tables.shape[1], NB, _dtype_code(q), PA_INT4)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = LIB.pa_decode_int4(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens),
-                            float(scale), int(num_kv_heads), ctypes.byref(dims), int(max_context_len),
-                            int(partition_tokens), _ptr(workspace), ws_bytes, _stream(stream))
-    _check(st)
+    st = LIB.pa_decode_int4(out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                            block_tables.data_ptr(), context_lens.data_ptr(), scale, num_kv_heads, dims,
+                            max_context_len, partition_tokens, _ptr(workspace), ws_bytes, _stream(stream))
+    if st != PA_OK:
+        _check(st)
     return out
 
 
@@ -479,49 +511,49 @@ def pa_reshape_and_cache(key: torch.Tensor, value: torch.Tensor, k_cache: torch.
     _check(st)
 
 
-def _check_rows(cache: torch.Tensor, slots: torch.Tensor, *rows: torch.Tensor) -> None:
-    """[tokens, KV heads, head_dim] rows that go with `slots` and a pool."""
-    _, Hk, _, D = _pool_shape(cache)
+def _rows_dims(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+               slots: torch.Tensor, num_heads: int):
+    """dims (by reference) of [tokens, KV heads, head_dim] rows that go with
+    `slots` and a pair of pools, after checking that they do."""
+    NB, Hk, B, D = _pool_shape(k_cache)
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must have one shape and dtype")
     if slots.dtype != torch.int64:
         raise TypeError("slot_mapping must be int64")
-    for t in rows:
-        if tuple(t.shape) != (slots.numel(), Hk, D):
-            raise ValueError(f"key and value must be [{slots.numel()}, {Hk}, {D}], got {tuple(t.shape)}")
-
-
-def _check_pools(k_cache: torch.Tensor, v_cache: torch.Tensor) -> None:
-    if k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
-        raise ValueError("k_cache and v_cache must have one shape and dtype")
+    shape = (slots.numel(), Hk, D)
+    if key.shape != shape or value.shape != shape:
+        raise ValueError(f"key and value must be {list(shape)}, got {list(key.shape)} and {list(value.shape)}")
+    kv = _kv_code(k_cache)
+    if value.dtype != key.dtype or (kv < PA_FP8_E4M3 and k_cache.dtype != key.dtype):
+        raise TypeError("key, value and a 16-bit cache must have one dtype")
+    return _dims_ref(0, num_heads, Hk, D, B, 0, NB, _dtype_code(key), kv)
 
 
 def pa_reshape_and_cache_int4(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                               slot_mapping: torch.Tensor, stream=None) -> None:
     """The 4-bit row of slot_mapping[t] = the codes, scale and low of key[t] (and value[t]) for slot >= 0."""
-    _need_cuda(key, value, k_cache, v_cache, slot_mapping)
     if not _is_int4(k_cache):
         raise TypeError("4-bit caches must be uint8 tensors of int4_cache_shape")
-    _check_pools(k_cache, v_cache)
-    _check_rows(k_cache, slot_mapping, key, value)
-    if value.dtype != key.dtype:
-        raise TypeError("key and value must have one dtype")
-    dims = cache_dims(k_cache, key.dtype)
-    _check(LIB.pa_reshape_and_cache_int4(_ptr(key), _ptr(value), _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping),
-                                         int(slot_mapping.numel()), ctypes.byref(dims), _stream(stream)))
+    dims = _rows_dims(key, value, k_cache, v_cache, slot_mapping, 0)
+    _on_device(key, value, k_cache, v_cache, slot_mapping)
+    _dense(key, value, k_cache, v_cache, slot_mapping)
+    st = LIB.pa_reshape_and_cache_int4(key.data_ptr(), value.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                       slot_mapping.data_ptr(), key.shape[0], dims, _stream(stream))
+    if st != PA_OK:
+        _check(st)
 
 
 def pa_gather_cache(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                     slot_mapping: torch.Tensor, k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> None:
     """key[t] (and value[t]) = the cached row of slot_mapping[t] in key's 16-bit
     dtype, for slot >= 0; other rows stay as they are."""
-    _need_cuda(key, value, k_cache, v_cache, slot_mapping)
-    _check_pools(k_cache, v_cache)
-    _check_rows(k_cache, slot_mapping, key, value)
-    if value.dtype != key.dtype or (_kv_code(k_cache) < PA_FP8_E4M3 and k_cache.dtype != key.dtype):
-        raise TypeError("key, value and a 16-bit cache must have one dtype")
-    dims = cache_dims(k_cache, key.dtype)
-    _check(LIB.pa_gather_cache(_ptr(key), _ptr(value), _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping),
-                               int(slot_mapping.numel()), ctypes.byref(dims), float(k_scale), float(v_scale),
-                               _stream(stream)))
+    dims = _rows_dims(key, value, k_cache, v_cache, slot_mapping, 0)
+    _on_device(key, value, k_cache, v_cache, slot_mapping)
+    _dense(key, value, k_cache, v_cache, slot_mapping)
+    st = LIB.pa_gather_cache(key.data_ptr(), value.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                             slot_mapping.data_ptr(), key.shape[0], dims, k_scale, v_scale, _stream(stream))
+    if st != PA_OK:
+        _check(st)
 
 
 # ---------------------------------------------------------------------------
@@ -546,31 +578,31 @@ def pa_rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "
     return inv_freq, magnitude.value
 
 
-def _token_rows(t: Optional[torch.Tensor], what: str) -> int:
+def _token_stride(t: torch.Tensor, what: str) -> int:
     """Elements between the tokens of a [tokens, heads, head_dim] tensor whose
     heads are contiguous (a view of a fused projection may have gaps between tokens)."""
-    if t is None:
-        return 0
-    if not t.is_cuda or t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-        raise ValueError(f"{what} must be a CUDA tensor [tokens, heads, head_dim] with contiguous heads")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    T, H, D = t.shape
+    st, sh, sd = t.stride()
+    if sd != 1 or (sh != D and H > 1):
+        raise ValueError(f"{what} must be [tokens, heads, head_dim] with contiguous heads")
+    return st if T > 1 else H * D
 
 
 def _rope_opts(inv_freq: torch.Tensor, positions: torch.Tensor, tokens: int, interleaved: bool, inverse: bool,
-               magnitude: float) -> pa_rope_opts:
-    _need_cuda(inv_freq, positions)
+               magnitude: float):
     if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
         raise TypeError("inv_freq must be float64 [rotary_dim / 2] (pa_rope_frequencies)")
     if positions.dtype != torch.int64 or positions.numel() != tokens:
         raise TypeError("positions must be int64, one per token")
-    return pa_rope_opts(inv_freq.data_ptr(), 2 * inv_freq.numel(), int(bool(interleaved)), int(bool(inverse)),
-                        float(magnitude))
+    return ctypes.byref(pa_rope_opts(inv_freq.data_ptr(), 2 * inv_freq.shape[0], 1 if interleaved else 0,
+                                     1 if inverse else 0, magnitude))
 
 
 def _same(a: Optional[torch.Tensor], b: Optional[torch.Tensor], what: str) -> None:
-    if (a is None) != (b is None):
-        raise ValueError(f"{what} and its output go together")
-    if a is not None and (a.shape != b.shape or a.dtype != b.dtype):
+    if a is None or b is None:
+        if a is not b:
+            raise ValueError(f"{what} and its output go together")
+    elif a.shape != b.shape or a.dtype != b.dtype:
         raise ValueError(f"{what} and its output must have one shape and dtype")
 
 
@@ -586,16 +618,18 @@ def pa_rope(q_out: Optional[torch.Tensor], q: Optional[torch.Tensor], k_out: Opt
     x = q if q is not None else k
     if x is None:
         raise ValueError("q or k is needed")
-    qs, ks = _token_rows(q, "q"), _token_rows(k, "k")
-    _need_cuda(q_out, k_out)
-    if q is not None and k is not None and (q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2] or
-                                            q.dtype != k.dtype):
+    _on_device(x, q, q_out, k, k_out, positions, inv_freq)
+    _dense(q_out, k_out, positions, inv_freq)
+    T, H, D = x.shape
+    if q is not None and k is not None and (k.shape[0] != T or k.shape[2] != D or q.dtype != k.dtype):
         raise ValueError("q and k must have the same tokens, head_dim and dtype")
-    opts = _rope_opts(inv_freq, positions, x.shape[0], interleaved, inverse, magnitude)
-    dims = make_dims(0, 0 if q is None else q.shape[1], 0 if k is None else k.shape[1], x.shape[2], 16, 0, 1,
-                     _dtype_code(x))
-    _check(LIB.pa_rope(_ptr(q_out), _ptr(q), _ptr(k_out), _ptr(k), _ptr(positions), int(x.shape[0]),
-                       ctypes.byref(dims), ctypes.byref(opts), qs, ks, _stream(stream)))
+    opts = _rope_opts(inv_freq, positions, T, interleaved, inverse, magnitude)
+    dims = _dims_ref(0, 0 if q is None else H, 0 if k is None else k.shape[1], D, 16, 0, 1, _dtype_code(x), 0)
+    st = LIB.pa_rope(_ptr(q_out), _ptr(q), _ptr(k_out), _ptr(k), positions.data_ptr(), T, dims, opts,
+                     0 if q is None else _token_stride(q, "q"), 0 if k is None else _token_stride(k, "k"),
+                     _stream(stream))
+    if st != PA_OK:
+        _check(st)
 
 
 def pa_rope_and_cache(q_out: Optional[torch.Tensor], q: Optional[torch.Tensor], key: torch.Tensor,
@@ -607,20 +641,19 @@ def pa_rope_and_cache(q_out: Optional[torch.Tensor], q: Optional[torch.Tensor], 
     negative slot are left out entirely.  q, key and value may be views of a
     fused projection; q may be None."""
     _same(q, q_out, "q")
-    qs, ks, vs = _token_rows(q, "q"), _token_rows(key, "key"), _token_rows(value, "value")
-    _need_cuda(q_out, k_cache, v_cache, slot_mapping)
-    _check_pools(k_cache, v_cache)
-    _check_rows(k_cache, slot_mapping, key, value)
-    if value.dtype != key.dtype or (_kv_code(k_cache) < PA_FP8_E4M3 and k_cache.dtype != key.dtype):
-        raise TypeError("key, value and a 16-bit cache must have one dtype")
-    if q is not None and (q.shape[0] != key.shape[0] or q.shape[2] != key.shape[2] or q.dtype != key.dtype):
+    T, _, D = key.shape
+    if q is not None and (q.shape[0] != T or q.shape[2] != D or q.dtype != key.dtype):
         raise ValueError("q and key must have the same tokens, head_dim and dtype")
-    opts = _rope_opts(inv_freq, positions, key.shape[0], interleaved, False, magnitude)
-    dims = cache_dims(k_cache, key.dtype)
-    dims.num_heads = 0 if q is None else q.shape[1]
-    _check(LIB.pa_rope_and_cache(_ptr(q_out), _ptr(q), _ptr(key), _ptr(value), _ptr(k_cache), _ptr(v_cache),
-                                 _ptr(slot_mapping), _ptr(positions), int(slot_mapping.numel()), ctypes.byref(dims),
-                                 ctypes.byref(opts), qs, ks, vs, float(k_scale), float(v_scale), _stream(stream)))
+    dims = _rows_dims(key, value, k_cache, v_cache, slot_mapping, 0 if q is None else q.shape[1])
+    _on_device(key, q, q_out, value, k_cache, v_cache, slot_mapping, positions, inv_freq)
+    _dense(q_out, k_cache, v_cache, slot_mapping, positions, inv_freq)
+    opts = _rope_opts(inv_freq, positions, T, interleaved, False, magnitude)
+    st = LIB.pa_rope_and_cache(_ptr(q_out), _ptr(q), key.data_ptr(), value.data_ptr(), k_cache.data_ptr(),
+                               v_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(), T, dims, opts,
+                               0 if q is None else _token_stride(q, "q"), _token_stride(key, "key"),
+                               _token_stride(value, "value"), k_scale, v_scale, _stream(stream))
+    if st != PA_OK:
+        _check(st)
 
 
 def pa_copy_blocks(k_caches: Sequence[torch.Tensor], v_caches: Sequence[torch.Tensor],
