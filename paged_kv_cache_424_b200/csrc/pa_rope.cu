@@ -94,7 +94,7 @@ __device__ __forceinline__ float2 up2(uint64_t v) {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
     return r;
 }
-// Two single-precision operations in one instruction, each rounded by itself.
+// Two single-precision operations in one instruction.
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -170,8 +170,10 @@ __device__ __forceinline__ uint32_t int4_codes(const float (&x)[8], float low, f
 __device__ __forceinline__ uint2 e4m3_codes(const float (&x)[8], float scale) {
     uint32_t u[2];
     if (divide2_fits(scale)) {
-        const float inv = __frcp_rn(scale), most = 512.f * scale;  // beyond it every quotient is clamped
-        const uint64_t y = pk2(inv, inv), mb = pk2(-scale, -scale);
+        // by -scale, with the codes' signs turned back at the end: so divided, a
+        // zero keeps its sign (by a positive number the last sum makes it +0)
+        const float inv = __frcp_rn(-scale), most = 512.f * scale;  // beyond it every quotient is clamped
+        const uint64_t y = pk2(inv, inv), mb = pk2(scale, scale);
         uint16_t h[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -179,8 +181,8 @@ __device__ __forceinline__ uint2 e4m3_codes(const float (&x)[8], float scale) {
             const float2 q = up2(divide2(pk2(a, b), y, mb));
             h[i] = float2_to_e4m3x2(q.x, q.y);
         }
-        u[0] = (uint32_t)h[0] | ((uint32_t)h[1] << 16);
-        u[1] = (uint32_t)h[2] | ((uint32_t)h[3] << 16);
+        u[0] = ((uint32_t)h[0] | ((uint32_t)h[1] << 16)) ^ 0x80808080u;
+        u[1] = ((uint32_t)h[2] | ((uint32_t)h[3] << 16)) ^ 0x80808080u;
     } else {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {

@@ -129,6 +129,31 @@ def test_gather_16bit_and_fp8(dtype, D):
             assert same_nan(got[live], want)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("D,Hk,T", [(64, 8, 20001), (128, 32, 3000), (64, 1, 70000)])
+def test_many_rows_written_and_read_back(dtype, D, Hk, T):
+    """More rows than the grids hold at once, a tenth of them padding: bit for bit."""
+    p = pa()
+    g = gen(T)
+    NB = T // 16 + 20
+    key, val = rand(g, (T, Hk, D), dtype, 3.0), rand(g, (T, Hk, D), dtype, 0.2)
+    slots = torch.randperm(NB * 16, generator=g, device="cuda")[:T]
+    slots = torch.where(torch.rand((T,), generator=g, device="cuda") < 0.1, torch.full_like(slots, -1), slots)
+    kc, vc = (torch.full(p.int4_cache_shape(NB, Hk, D), 0x5A, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ek, ev = kc.clone(), vc.clone()
+    p.pa_reshape_and_cache_int4(key, val, kc, vc, slots)
+    a, b = torch.full_like(key, 5.0), torch.full_like(key, 5.0)
+    p.pa_gather_cache(a, b, kc, vc, slots)
+    torch.cuda.synchronize()
+    live = slots >= 0
+    for pool, want, x, back in ((kc, ek, key, a), (vc, ev, val, b)):
+        codes, ends = ref.quantise(x)
+        ref.put_rows(want, codes, ends, slots)
+        assert torch.equal(pool, want)
+        values = (codes.float() * ends[..., :1].float() + ends[..., 1:].float()).to(dtype)
+        assert torch.equal(back[live], values[live]) and bool((back[~live] == 5.0).all())
+
+
 def test_gather_flags_slots_past_the_pool():
     p = pa()
     pool = torch.zeros(p.int4_cache_shape(2, 4, 64), dtype=torch.uint8, device="cuda")
@@ -257,6 +282,21 @@ def test_random_shapes(seed):
         b = batch(g, lens, int(rng.choice([1, 3, 8])), group, D, dtype, q_len=q_len, level=float(rng.choice([0.01, 0.3, 2.0])))
         check(*b, ref.scale_of(D), f"{lens}", q_len=q_len, window=int(rng.choice([0, 0, 1, 50, 1000])), ext=True,
               P=int(rng.choice([0, 16, 64, 512])), ks=float(rng.choice([1.0, 0.5])), vs=float(rng.choice([1.0, 3.0])))
+
+
+@pytest.mark.parametrize("S,Hk,most", [(4097, 1, 300), (5000, 2, 130), (300, 4, 100), (4096, 2, 200)])
+def test_many_sequences(S, Hk, most):
+    """Batches past the limit of the shared-out kernel, at it, and of short
+    contexts; 60 sequences checked, the first and last among them."""
+    g = gen(S)
+    lens = [int(n) for n in torch.randint(0, most, (S,), generator=g, device="cuda")]
+    lens[-1] = most
+    q, kc, vc, tables, cl = batch(g, lens, Hk, 4, 64, torch.float16)
+    out = run(q, kc, vc, tables, cl, 0.125)
+    some = torch.cat((torch.randperm(S, generator=g, device="cuda")[:58], torch.tensor([0, S - 1], device="cuda")))
+    want, slack = ref.attend(q[some], kc, vc, tables[some], cl[some], 0.125)
+    ref.near(out[some], want, slack, f"{S} sequences")
+    assert bool(out.isfinite().all())
 
 
 def test_extreme_scales_and_queries():

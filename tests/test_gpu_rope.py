@@ -248,6 +248,52 @@ def test_value_write_equals_the_unrotated_write(kind):
     assert torch.equal(a, c) and torch.equal(b, d)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("scale", [1.0, 0.0123, 3.7, 1e-30, 3e-38, 1e30, 1.9999999, 2.0 ** -90])
+def test_fp8_codes_of_every_16bit_value(dtype, scale):
+    """The value half quantises every 16-bit pattern as pa_reshape_and_cache_fp8
+    does (a correctly rounded quotient, whichever way it is formed), NaN as NaN."""
+    p = pa()
+    v = torch.arange(65536, device="cuda").to(torch.int16).view(dtype).view(256, 2, 128)
+    pools = [torch.zeros((16, 2, 16, 128), dtype=torch.uint8, device="cuda") for _ in range(4)]
+    slots, pos = torch.arange(256, device="cuda"), torch.zeros(256, dtype=torch.int64, device="cuda")
+    k = torch.zeros_like(v)
+    s = float(torch.tensor(scale, dtype=torch.float32))
+    p.pa_rope_and_cache(None, None, k, v, pools[0], pools[1], slots, pos, freqs(128), k_scale=1.0, v_scale=s)
+    p.pa_reshape_and_cache_fp8(k, v, pools[2], pools[3], slots, 1.0, s)
+    torch.cuda.synchronize()
+    nan = (pools[3] & 0x7F) == 0x7F
+    assert torch.equal(nan, (pools[1] & 0x7F) == 0x7F) and torch.equal(pools[1][~nan], pools[3][~nan])
+
+
+@pytest.mark.parametrize("kind", ["none", "16", "int4"])
+@pytest.mark.parametrize("H,Hk,D,R,inter", [(1, 1, 64, 64, False), (3, 1, 128, 64, True), (32, 8, 128, 20, False), (32, 8, 128, 128, False)])
+def test_many_tokens(kind, H, Hk, D, R, inter):
+    """More tokens than CTAs: each walks over several, padding among them."""
+    p = pa()
+    g = gen(H + D)
+    T, NB = 3001, 200
+    f = freqs(R)
+    qkv = rand(g, (T, H + 2 * Hk, D), torch.bfloat16)
+    q, k, v = qkv[:, :H], qkv[:, H:H + Hk], qkv[:, H + Hk:]
+    pos = torch.randint(0, 30000, (T,), generator=g, device="cuda")
+    if kind == "none":
+        check_rope(q, k, pos, f, inter)
+        return
+    slots = torch.randperm(NB * 16, generator=g, device="cuda")[:T]
+    slots = torch.where(torch.rand((T,), generator=g, device="cuda") < 0.4, torch.full_like(slots, -1), slots)
+    kc, vc = pools_of(kind, NB, Hk, D, torch.bfloat16, g)
+    qo = torch.full((T, H, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    p.pa_rope_and_cache(qo, q, k, v, kc, vc, slots, pos, f, interleaved=inter)
+    torch.cuda.synchronize()
+    live = slots >= 0
+    at = slots[live]
+    assert bool((qo[~live] == 7.0).all())
+    ref.near(qo[live], ref.rotate(q, pos, f, inter)[live], ref.rotate_bound(q, f, inter)[live], "q")
+    check_cache_row(kind, kc, at, ref.rotate(k, pos, f, inter)[live], ref.rotate_bound(k, f, inter)[live], 1.0, "K")
+    check_cache_row(kind, vc, at, v.double()[live], torch.zeros_like(v.double()[live]), 1.0, "V")
+
+
 def test_slot_past_the_pool_is_flagged_and_skipped():
     g = gen(9)
     p = pa()
