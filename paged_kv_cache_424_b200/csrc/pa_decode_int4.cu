@@ -753,19 +753,22 @@ __global__ void __launch_bounds__(kWarps * 32, int4_ctas_per_sm(RT))
 }
 
 // Joins the pieces of contexts that no warp held whole: out = sum_i 2^(lse_i -
-// M) o_i / sum_i 2^(lse_i - M), M = max lse.  CTA = (4 / kRowWarps query rows
-// of a sequence): kRowWarps warps share a row's pieces (1 where contexts have
-// few, 4 where they have many).
-template <typename T, int D, int kRowWarps>
+// M) o_i / sum_i 2^(lse_i - M), M = max lse.  CTA = (4 kRows / kRowWarps query
+// rows of a sequence).  Where contexts have few pieces a warp takes kRows = 4
+// neighbouring rows of one KV head, whose pieces and places are the same (1
+// where the KV head's rows are no multiple of 4); where they have many, four
+// warps share one row's pieces.
+template <typename T, int D, int kRowWarps, int kRows>
 __global__ void __launch_bounds__(128) merge_int4_kernel(const DecodeParams p, const int32_t *places, const int teams, const int team_bits) {
     using E = Elem<T>;
     constexpr int kV = D / 32;
-    __shared__ float red[4][D + 1];
+    static_assert(kRowWarps == 1 || kRows == 1, "several warps share one row");
+    __shared__ float red[kRowWarps == 4 ? 4 : 1][D + 1];
     const int s = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_launch_dependents();
     const Int4Seq seq = int4_seq(p, s, false);
     const int rows = p.group * p.q_len;
-    const int row = blockIdx.x * (4 / kRowWarps) + warp / kRowWarps;  // query row of the sequence, KV head by KV head
+    const int row = (blockIdx.x * (4 / kRowWarps) + warp / kRowWarps) * kRows;  // query row of the sequence, KV head by KV head
     const bool real = row < p.num_kv_heads * rows;
     const int kvh = real ? row / rows : 0, h = real ? row % rows : 0;
     pdl_wait();
@@ -773,65 +776,79 @@ __global__ void __launch_bounds__(128) merge_int4_kernel(const DecodeParams p, c
     const int at = places[s] + (kvh >> team_bits) * (kStartCost + seq.n) + kStartCost;
     const int ta = at / share;
     const int pieces = seq.n == 0 || !real ? 0 : (at + seq.n - 1) / share - ta + 1;
-    if (kRowWarps == 4 ? pieces <= 1 : __all_sync(0xffffffffu, pieces <= 1)) return;  // written by its warp
+    if (pieces <= 1) return;  // written by its warp; with four warps to a row it is all four that leave
     // piece i: the first in the second slot of its warp, the others in the first
     const int member = kvh & ((1 << team_bits) - 1);
     auto slot = [&](int i) -> int64_t { return (2 * (((int64_t)(ta + i) << team_bits) + member) + (i == 0 ? 1 : 0)) * rows + h; };
-    float M = -INFINITY;
-    for (int i = lane; i < pieces; i += 32) M = fmaxf(M, p.ws_lse[slot(i)]);
-    float acc[kV] = {}, wsum = 0.f;
-    constexpr int kInFlight = 4;
+    float M[kRows], acc[kRows][kV] = {}, wsum[kRows] = {};
+#pragma unroll
+    for (int n = 0; n < kRows; ++n) M[n] = -INFINITY;
+    for (int i = lane; i < pieces; i += 32)
+#pragma unroll
+        for (int n = 0; n < kRows; ++n) M[n] = fmaxf(M[n], p.ws_lse[slot(i) + n]);
+    constexpr int kInFlight = kRows == 4 ? 2 : 4;
     bool first = true;
     for (int i0 = warp % kRowWarps; i0 < pieces || first; i0 += kRowWarps * kInFlight) {
-        float lse[kInFlight], v[kInFlight][kV];
+        float lse[kInFlight][kRows], v[kInFlight][kRows][kV];
 #pragma unroll
         for (int k = 0; k < kInFlight; ++k) {  // every piece was written: no need to look at its lse first
             const int i = i0 + k * kRowWarps;
-            lse[k] = i < pieces ? p.ws_lse[slot(i)] : -INFINITY;
+            const int64_t at_row = slot(i);
 #pragma unroll
-            for (int e = 0; e < kV; e += 2) {
-                const float2 f = i < pieces ? *reinterpret_cast<const float2 *>(p.ws_o + slot(i) * D + lane * kV + e)
-                                            : make_float2(0.f, 0.f);
-                v[k][e] = f.x;
-                v[k][e + 1] = f.y;
+            for (int n = 0; n < kRows; ++n) {
+                lse[k][n] = i < pieces ? p.ws_lse[at_row + n] : -INFINITY;
+                const float *src = p.ws_o + (at_row + n) * D + lane * kV;
+                if constexpr (kV == 4) {
+                    const float4 f = i < pieces ? *reinterpret_cast<const float4 *>(src) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    v[k][n][0] = f.x, v[k][n][1] = f.y, v[k][n][2] = f.z, v[k][n][3] = f.w;
+                } else {
+                    const float2 f = i < pieces ? *reinterpret_cast<const float2 *>(src) : make_float2(0.f, 0.f);
+                    v[k][n][0] = f.x, v[k][n][1] = f.y;
+                }
             }
         }
         if (first) {
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+            for (int n = 0; n < kRows; ++n)
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) M[n] = fmaxf(M[n], __shfl_xor_sync(0xffffffffu, M[n], o));
             first = false;
         }
 #pragma unroll
-        for (int k = 0; k < kInFlight; ++k) {
-            const float w = lse[k] == -INFINITY ? 0.f : exp2f(lse[k] - M);
-            wsum += w;
+        for (int k = 0; k < kInFlight; ++k)
 #pragma unroll
-            for (int e = 0; e < kV; ++e) acc[e] = fmaf(w, v[k][e], acc[e]);
-        }
+            for (int n = 0; n < kRows; ++n) {
+                const float w = lse[k][n] == -INFINITY ? 0.f : ex2(lse[k][n] - M[n]);
+                wsum[n] += w;
+#pragma unroll
+                for (int e = 0; e < kV; ++e) acc[n][e] = fmaf(w, v[k][n][e], acc[n][e]);
+            }
     }
     if constexpr (kRowWarps == 4) {
 #pragma unroll
-        for (int e = 0; e < kV; ++e) red[warp][lane * kV + e] = acc[e];
-        if (lane == 0) red[warp][D] = wsum;
+        for (int e = 0; e < kV; ++e) red[warp][lane * kV + e] = acc[0][e];
+        if (lane == 0) red[warp][D] = wsum[0];
         __syncthreads();
         if (warp != 0) return;
-        wsum = 0.f;
+        wsum[0] = 0.f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) wsum += red[k][D];
+        for (int k = 0; k < 4; ++k) wsum[0] += red[k][D];
 #pragma unroll
         for (int e = 0; e < kV; ++e) {
-            acc[e] = 0.f;
+            acc[0][e] = 0.f;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) acc[e] += red[k][lane * kV + e];
+            for (int k = 0; k < 4; ++k) acc[0][e] += red[k][lane * kV + e];
         }
     }
-    if (pieces <= 1) return;
-    const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
-    T *dst = reinterpret_cast<T *>(p.out) + query_row(p, s, kvh, h) * D + lane * kV;
 #pragma unroll
-    for (int e = 0; e < kV; e += 2) {
-        const typename E::T2 a = {E::from_float(acc[e] * inv), E::from_float(acc[e + 1] * inv)};
-        *reinterpret_cast<typename E::T2 *>(dst + e) = a;
+    for (int n = 0; n < kRows; ++n) {
+        const float inv = wsum[n] == 0.f ? 0.f : 1.f / wsum[n];
+        T *dst = reinterpret_cast<T *>(p.out) + query_row(p, s, kvh, h + n) * D + lane * kV;
+#pragma unroll
+        for (int e = 0; e < kV; e += 2) {
+            const typename E::T2 a = {E::from_float(acc[n][e] * inv), E::from_float(acc[n][e + 1] * inv)};
+            *reinterpret_cast<typename E::T2 *>(dst + e) = a;
+        }
     }
 }
 
@@ -856,11 +873,12 @@ cudaError_t launch_int4_t(const DecodeParams &p, int32_t *places, int ctas, cuda
     e = launch_pdl(kern, dim3(ctas), dim3(kWarps * 32), kSmem, stream, p, places, team_bits);
     if (e != cudaSuccess) return e;
     // pieces a context may have: many on few sequences
-    const int rows = p.num_heads * p.q_len;
+    const int rows = p.num_heads * p.q_len, four = p.group * p.q_len % 4 == 0;
     const bool many = (int64_t)ctas * kWarps > 8 * (int64_t)p.num_seqs * p.num_kv_heads;
-    const dim3 grid(many ? rows : (rows + 3) / 4, p.num_seqs);
-    return many ? launch_pdl(merge_int4_kernel<T, D, 4>, grid, dim3(128), 0, stream, p, (const int32_t *)places, teams, team_bits)
-                : launch_pdl(merge_int4_kernel<T, D, 1>, grid, dim3(128), 0, stream, p, (const int32_t *)places, teams, team_bits);
+    const int32_t *at = places;
+    if (many) return launch_pdl(merge_int4_kernel<T, D, 4, 1>, dim3(rows, p.num_seqs), dim3(128), 0, stream, p, at, teams, team_bits);
+    if (four) return launch_pdl(merge_int4_kernel<T, D, 1, 4>, dim3((rows + 15) / 16, p.num_seqs), dim3(128), 0, stream, p, at, teams, team_bits);
+    return launch_pdl(merge_int4_kernel<T, D, 1, 1>, dim3((rows + 3) / 4, p.num_seqs), dim3(128), 0, stream, p, at, teams, team_bits);
 }
 
 template <typename T, int D>
