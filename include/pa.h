@@ -128,7 +128,9 @@ size_t pa_decode_workspace_size(const pa_dims *dims, int32_t max_context_len,
 
 /*
  * Number of KV partitions per sequence pa_decode will use (1 = unsplit),
- * or a negative pa_status for invalid arguments.
+ * or a negative pa_status for invalid arguments.  For a 4-bit cache with
+ * partition_tokens = 0, whose contexts are cut where equal shares of the batch
+ * end, the most pieces that one context can fall into.
  */
 int32_t pa_decode_num_partitions(const pa_dims *dims, int32_t max_context_len,
                                  int32_t partition_tokens);
@@ -281,13 +283,18 @@ pa_status pa_decode_ext(void *out, const void *q, const void *k_cache, const voi
  * Decode attention over 4-bit caches (dims->kv_dtype == PA_INT4): pa_decode
  * with K_s[j] = code * scale + low of the row (j, KV head), V_s[j] likewise;
  * about a quarter of the bytes of a 16-bit cache.  Every group size and
- * head_dim runs on one kernel that feeds the codes to the matrix units as
- * exact integers: the query is rounded to 11 significant bits under a
- * power-of-two factor per row (exact for any 16-bit q within 2^22 of the
- * row's largest |q|) and the softmax weight times the V scale to fp16
- * (|error| <= 2^-11 of the weight), logits, sums and the output in fp32.
- * partition_tokens: 0 = automatic.  Workspace as from
- * pa_decode_workspace_size with the same dims.
+ * head_dim runs on kernels that feed the codes to the matrix units as exact
+ * integers.  The query is rounded to integers under a power-of-two factor per
+ * row: every element to within 2^-14 of the row's largest |q| (exact for fp16
+ * elements within 2^4 of it, for bf16 ones within 2^7), and the products with
+ * the codes are exact.  The softmax weight times the V scale is rounded to
+ * fp16, with up to 4 query rows per KV head to two fp16 parts (22 bits); what
+ * the rounding of more rows takes is given back at the middle code, so its
+ * error is at most 2^-11 of the weight times 7.5 codes.  Logits, sums and the
+ * output are fp32.  A row that attends to a row of NaN is NaN.
+ * partition_tokens: 0 = automatic: equal shares of all blocks of the batch,
+ * whatever the lengths (one context is not cut at fixed positions).
+ * Workspace as from pa_decode_workspace_size with the same dims.
  */
 pa_status pa_decode_int4(void *out, const void *q, const void *k_cache, const void *v_cache,
                          const int32_t *block_tables, const int32_t *context_lens, float scale,

@@ -96,6 +96,14 @@ def random_pool(gen, NB, Hk, D, spread=0.3, level=0.3):
     return pool
 
 
+def query_integers(q):
+    """Rows [.., D] as the kernel takes them: integers (largest in 2^13 .. 2^14 - 1) under a power of two per row."""
+    q = q.double()
+    _, e = torch.frexp(q.abs().amax(-1, keepdim=True))
+    up = torch.ldexp(torch.ones_like(q[..., :1]), (14 - e).clamp(max=120))
+    return torch.round(q * up).clamp(max=16383.0) / up
+
+
 def attend(q, k_pool, v_pool, tables, lens, scale, q_len=1, window=0, k_scale=1.0, v_scale=1.0):
     """float64 attention [S, q_len, H, D] and, per output, the bound of the
     kernel's error before the output's own rounding.
@@ -111,7 +119,10 @@ def attend(q, k_pool, v_pool, tables, lens, scale, q_len=1, window=0, k_scale=1.
         with 2 (D + 8) half steps of fp32 for sums, products, the query's own
         scaling and the exponential, d = 2 (D + 8) 2^-24 c (15 max|s| +
         max|l|) sum|q| plus 2^-21 of the largest |logit| and as much again
-        for the exponential.  Moving each logit by at most d moves the output by at most
+        for the exponential.  The query enters as integers under a power of
+        two (`query_integers`): with e_i what that takes from element i, a
+        logit moves by |sum_i e_i (s u_i + l)| <= (15 max|s| + max|l|)
+        c sum|e|.  Moving each logit by at most d moves the output by at most
         (e^(2 d) - 1) max|v|.
       - sums of weights and outputs over n tokens in fp32: (n / 16 + 64) half
         steps at the most of the sum of magnitudes, max(15 |s| + |l|).
@@ -141,7 +152,8 @@ def attend(q, k_pool, v_pool, tables, lens, scale, q_len=1, window=0, k_scale=1.
             sk, lk = ke[b, :, o, 0].abs().amax(0) * k_scale, ke[b, :, o, 1].abs().amax(0) * k_scale
             sv, lv = ve[b, :, o, 0].abs().amax(0) * v_scale, ve[b, :, o, 1].abs().amax(0) * v_scale
             qs = qq.abs().sum(-1) * abs(scale)                   # [Hk, g]
-            d = 2 * (D + 8) * 2.0 ** -24 * (15 * sk + lk)[:, None] * qs + 2.0 ** -20 * x.abs().amax(-1)
+            lost = (qq - query_integers(qq)).abs().sum(-1) * abs(scale)
+            d = (15 * sk + lk)[:, None] * (2 * (D + 8) * 2.0 ** -24 * qs + lost) + 2.0 ** -20 * x.abs().amax(-1)
             top = (15 * sv + lv)[:, None]
             e = (2.0 ** -11 + 2.0 ** -20) * 7.5 * sv[:, None] + torch.expm1(2 * d) * top + \
                 (len(at) / 16 + 64) * 2.0 ** -24 * top
