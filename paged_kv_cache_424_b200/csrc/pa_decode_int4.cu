@@ -562,11 +562,9 @@ __global__ void __launch_bounds__(kWarps * 32, int4_ctas_per_sm(RT)) decode_int4
     const int part = blockIdx.x, kvh = blockIdx.y;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, q = lane & 3;
     pdl_launch_dependents();
-    // Order and lengths are read before the wait for the kernel in front (no
-    // kernel of this library writes them), q and the caches after.
+    pdl_wait();
     const int s = scheduled_seq(p, blockIdx.z, part == 0 && kvh == 0 && tid == 0);
     const SeqSplit sp = s < 0 ? SeqSplit{0, 0, 0, 0} : seq_split(p, s, part == 0 && kvh == 0 && tid == 0);
-    pdl_wait();
     if (part >= sp.nparts) return;  // s < 0 too
     const int rows = p.group * p.q_len;
     T *out = reinterpret_cast<T *>(p.out);
@@ -651,9 +649,8 @@ __global__ void __launch_bounds__(kWarps * 32, int4_ctas_per_sm(RT))
     pdl_launch_dependents();
     const uint32_t ring = smem_addr(smem) + warp * kStages * 4 * int4_chunk_bytes(D);
     const int groups = p.num_kv_heads >> team_bits, member = warp & ((1 << team_bits) - 1);
+    pdl_wait();
     // places of all sequences: each thread sums a run of them, then a scan
-    // (before the wait for the kernel in front: no kernel of this library
-    // writes lengths)
     const int per = (p.num_seqs + kThreads - 1) / kThreads, s0 = min(tid * per, p.num_seqs), s1 = min(s0 + per, p.num_seqs);
     const bool report = blockIdx.x == 0;
     int sum = 0;
@@ -672,7 +669,6 @@ __global__ void __launch_bounds__(kWarps * 32, int4_ctas_per_sm(RT))
     const int total = (int)chunk_end[kThreads - 1];
     const int teams = ((int)gridDim.x * kWarps) >> team_bits, share = int4_share(total, teams);
     if (blockIdx.x == 0) {
-        pdl_wait();  // an earlier call's merge may still read them
         int at = scan - sum;
         for (int s = s0; s < s1; ++s) {
             places[s] = at;
@@ -686,7 +682,6 @@ __global__ void __launch_bounds__(kWarps * 32, int4_ctas_per_sm(RT))
     const int64_t begin = (int64_t)(me >> team_bits) * share;
     int x = (int)min((int64_t)total, begin);
     const int xend = (int)min((int64_t)total, begin + share);
-    pdl_wait();
     if (x >= xend) return;
     // the sequence of place x: the thread whose run holds it, then its run
     int c = 0;
@@ -766,12 +761,12 @@ __global__ void __launch_bounds__(128) merge_int4_kernel(const DecodeParams p, c
     __shared__ float red[kRowWarps == 4 ? 4 : 1][D + 1];
     const int s = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_launch_dependents();
+    pdl_wait();
     const Int4Seq seq = int4_seq(p, s, false);
     const int rows = p.group * p.q_len;
     const int row = (blockIdx.x * (4 / kRowWarps) + warp / kRowWarps) * kRows;  // query row of the sequence, KV head by KV head
     const bool real = row < p.num_kv_heads * rows;
     const int kvh = real ? row / rows : 0, h = real ? row % rows : 0;
-    pdl_wait();
     const int share = int4_share(places[p.num_seqs], teams);
     const int at = places[s] + (kvh >> team_bits) * (kStartCost + seq.n) + kStartCost;
     const int ta = at / share;

@@ -286,9 +286,8 @@ __global__ void __launch_bounds__(kThreads, 8) rope_kernel(const RopeParams p) {
     const int total = H + (kCache == kCacheNone ? Hk : 2 * Hk);
     const int first = (int)blockIdx.y * kRows, step = kRows * (int)gridDim.y;  // of the CTA's passes
     const int mine = tid / LPR;                                                // this lane's row in a pass
-    // positions, slots and frequencies are no kernel of this library's output:
-    // the first token's sines are computed before the wait for the kernel in
-    // front, a later one's while the token before it is worked on
+    pdl_wait();  // the caller's last kernel may have written any input, positions and slots too
+    // a token's sines are computed while the token before it is worked on
     const double freq = tid < half ? p.inv_freq[tid] * 0.15915494309189533576888 : 0.0;
     auto sines = [&](int t, int buf) {
         if (tid >= half) return;
@@ -312,10 +311,11 @@ __global__ void __launch_bounds__(kThreads, 8) rope_kernel(const RopeParams p) {
     };
     int t = blockIdx.x, buf = 0;
     int64_t slot = slot_of(t);
-    if (slot >= 0) sines(t, 0);
-    pdl_wait();
     uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (slot >= 0) load(t, first + mine, w);
+    if (slot >= 0) {
+        load(t, first + mine, w);
+        sines(t, 0);
+    }
     for (;;) {
         const int t2 = t + (int)gridDim.x;
         const bool more = t2 < p.num_tokens;
@@ -440,8 +440,8 @@ __global__ void __launch_bounds__(kThreads) write_int4_kernel(const RopeParams p
         w[0] = reinterpret_cast<const uint4 *>(src)[2 * j];
         w[1] = reinterpret_cast<const uint4 *>(src)[2 * j + 1];
     };
-    int64_t slot = slot_of(base + mine);
     pdl_wait();
+    int64_t slot = slot_of(base + mine);
     uint4 w[2];
     load(base + mine, slot, w);
     for (; base < rows; base += groups) {

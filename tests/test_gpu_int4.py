@@ -551,3 +551,65 @@ def test_graphs_with_a_shared_workspace_and_streams():
             call(x, o, w, st)
         torch.cuda.synchronize()
         assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+
+
+def test_inputs_written_by_the_kernel_in_front():
+    """A captured loop whose torch kernels change positions, slots, lengths and
+    queries right in front of the calls, two batches sharing a workspace with
+    automatic shares: every step as a synchronised eager one gives it."""
+    p = pa()
+    g = gen(33)
+    steps, H, Hk, D = 24, 8, 2, 128
+    f, _ = p.pa_rope_frequencies(D)
+    f = f.cuda()
+    lens0 = [[2000, 130, 1], [900, 700, 33, 5, 256]]
+    sets = []
+    for lens in lens0:
+        S = len(lens)
+        rows = 2064 // 16
+        NB = S * rows
+        kc, vc = ref.random_pool(g, NB, Hk, D), ref.random_pool(g, NB, Hk, D)
+        tables = torch.randperm(NB, generator=g, device="cuda").int().view(S, rows)
+        news = [rand(g, (steps, S, h, D), torch.bfloat16) for h in (H, Hk, Hk)]
+        sets.append(dict(kc=kc, vc=vc, tables=tables, news=news, S=S, first=torch.tensor(lens, dtype=torch.int32, device="cuda")))
+    size = max(p.pa_decode_workspace_size(p.dims_of(x["news"][0][0], x["kc"], x["tables"]), 2064) for x in sets)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+
+    def loop(sync):
+        outs = []
+        state = []
+        for x in sets:
+            state.append(dict(kc=x["kc"].clone(), vc=x["vc"].clone(), lens=x["first"].clone(), pos=torch.zeros(x["S"], dtype=torch.int64, device="cuda"),
+                              slots=torch.zeros(x["S"], dtype=torch.int64, device="cuda"), q=torch.empty_like(x["news"][0][0]),
+                              rq=torch.empty_like(x["news"][0][0]), k=torch.empty_like(x["news"][1][0]), v=torch.empty_like(x["news"][1][0])))
+
+        def body():
+            for t in range(steps):
+                for x, s in zip(sets, state):
+                    for name, new in zip("qkv", x["news"]):
+                        s[name].copy_(new[t])
+                    at = s["lens"].long()
+                    s["slots"].copy_(x["tables"].gather(1, (at // 16)[:, None])[:, 0].long() * 16 + at % 16)
+                    s["pos"].copy_(at)
+                    p.pa_rope_and_cache(s["rq"], s["q"], s["k"], s["v"], s["kc"], s["vc"], s["slots"], s["pos"], f)
+                    s["lens"].add_(1)
+                    out = torch.empty_like(s["q"])
+                    if sync:
+                        torch.cuda.synchronize()
+                    p.pa_decode_int4(out, s["rq"], s["kc"], s["vc"], x["tables"], s["lens"], D ** -0.5, Hk, 2064, 0, ws)
+                    if sync:
+                        torch.cuda.synchronize()
+                    outs.append(out)
+        return body, outs, state
+
+    body, want, _ = loop(True)
+    body()
+    body, got, _state = loop(False)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        body()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert len(got) == len(want) == 2 * steps
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
