@@ -338,8 +338,8 @@ pa_status pa_gather_cache(void *key, void *value, const void *k_cache, const voi
  * -theta: with the same m that is the transpose of the forward map, so it
  * takes the gradient of a rotated row to the gradient of the row.  Angles and
  * their sines are computed in fp64 (a position of 10^6 keeps them exact to
- * fp32), m cos and m sin are rounded to fp32 and applied in fp32; results are
- * rounded once.
+ * fp32), m cos and m sin are rounded to fp32 and applied in fp32, the two
+ * products and their sum each rounded; results are rounded once to their type.
  */
 typedef struct pa_rope_opts {
     const double *inv_freq; /* DEVICE, [rotary_dim / 2]; see pa_rope_frequencies */

@@ -105,12 +105,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-
-__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
@@ -351,10 +345,13 @@ __global__ void __launch_bounds__(kThreads, 8) rope_kernel(const RopeParams p) {
                         for (int i = 0; i < 2; ++i) {
                             const int e = 4 * k + 2 * i;
                             const uint64_t a = pk2(xa[e], xa[e + 1]), b = pk2(xb[e], xb[e + 1]);
-                            const float2 ya = up2(sub2(mul2(a, c2[i]), mul2(b, s2[i])));
-                            const float2 yb = up2(add2(mul2(b, c2[i]), mul2(a, s2[i])));
-                            xa[e] = ya.x, xa[e + 1] = ya.y;
-                            xb[e] = yb.x, xb[e + 1] = yb.y;
+                            // sums of two single operations each: the compiler makes a packed
+                            // multiply and the packed sum behind it one fused operation, which
+                            // rounds once where the definition rounds twice
+                            const float2 ac = up2(mul2(a, c2[i])), bs = up2(mul2(b, s2[i]));
+                            const float2 bc = up2(mul2(b, c2[i])), as = up2(mul2(a, s2[i]));
+                            xa[e] = __fsub_rn(ac.x, bs.x), xa[e + 1] = __fsub_rn(ac.y, bs.y);
+                            xb[e] = __fadd_rn(bc.x, as.x), xb[e + 1] = __fadd_rn(bc.y, as.y);
                         }
                     }
                 }

@@ -98,6 +98,31 @@ def test_no_tokens_and_empty_tail():
     assert not pool.any()
 
 
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_products_and_sums_are_rounded_one_by_one(dtype, inter):
+    """Bit for bit the fp32 form with every operation rounded (a product fused
+    into the sum moves about one fp16 result in 50,000).  Frequencies are powers
+    of two and positions small, so that the angles are exact and the sines
+    of two fp64 implementations, which agree to about 1e-15, round to one fp32
+    number but for about one in 10^7."""
+    g = gen(77)
+    T, H, D = 512, 64, 128
+    q = rand(g, (T, H, D), dtype, 2.0)
+    f = torch.ldexp(torch.ones(D // 2, dtype=torch.float64, device="cuda"), -(torch.arange(D // 2, device="cuda") // 8).int())
+    pos = torch.arange(T, device="cuda") % 8
+    out = torch.empty_like(q)
+    pa().pa_rope(out, q, None, None, pos, f, interleaved=inter)
+    angle = pos.double()[:, None] * f
+    co, si = angle.cos().float()[:, None], angle.sin().float()[:, None]
+    x = q.float()
+    a, b = (x[..., 0::2], x[..., 1::2]) if inter else (x[..., :D // 2], x[..., D // 2:])
+    ac, bs, bc, as_ = a * co, b * si, b * co, a * si
+    turned = (ac - bs, bc + as_)
+    want = (torch.stack(turned, -1).flatten(-2) if inter else torch.cat(turned, -1)).to(dtype)
+    assert torch.equal(out, want)
+
+
 def test_positions_far_away():
     """fp32 angles would be off by 0.06 rad at 10^6; fp64 ones are off by less
     than 2^-52 * 10^6 * 3 = 7e-10 there, far below fp32's half step.  At 2^31
