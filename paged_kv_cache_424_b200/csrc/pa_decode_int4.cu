@@ -206,26 +206,34 @@ struct Int4Warp {
                 (void)frexpf(mx, &e);  // mx in [2^(e-1), 2^e)
                 e = min(14 - e, 120);  // mx 2^e in [2^13, 2^14)
             }
+            // 1.5 2^23 + v holds the integer v in its low bits.  The largest |q| is
+            // a 16-bit number, so its v is exact and at most 16376, and with it
+            // every |v|: the high part fits s8.  (A row that is not fine may give
+            // anything: its factor is NaN.)
+            constexpr float kInt = 12582912.f;
             const float up = ldexpf(1.f, e);
-            int sum = 0;
+            const uint32_t part_mask = (r & 1) ? 0x7f7f7f7fu : 0xffffffffu;
+            const int part_shift = (r & 1) ? 0 : 7;
+            uint32_t sum = 0;
 #pragma unroll
             for (int w = 0; w < KW; ++w)
 #pragma unroll
                 for (int odd = 0; odd < 2; ++odd) {
-                    uint32_t bytes = 0;
+                    uint32_t v[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int v = fine ? min(__float2int_rn(y[8 * w + 2 * i + odd] * up), 16383) : 0;
-                        sum += v;
-                        bytes |= (uint32_t)(((r & 1) ? v & 127 : v >> 7) & 255) << (8 * i);
+                        const uint32_t k = __float_as_uint(fmaf(y[8 * w + 2 * i + odd], up, kInt));
+                        sum += k;
+                        v[i] = k >> part_shift;
                     }
-                    qb[n][2 * w + odd] = bytes;
+                    qb[n][2 * w + odd] = __byte_perm(__byte_perm(v[0], v[1], 0x0040), __byte_perm(v[2], v[3], 0x0040), 0x5410) & part_mask;
                 }
+            sum -= (uint32_t)(D / 4) * 0x4b400000u;  // the constant's bits
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
             const float f = fine ? ldexpf(p.scale_log2, -e) : NAN;
             fac[n] = __shfl_sync(0xffffffffu, f, 8 * q) * (kOneSum ? 1.f : 0.0625f);
-            off_q[n] = __shfl_sync(0xffffffffu, (float)sum * f, 8 * q);
+            off_q[n] = __shfl_sync(0xffffffffu, (float)(int)sum * f, 8 * q);
             m[n] = -INFINITY;
             l[n] = z[n] = zw[n] = 0.f;
             if constexpr (kMasked) row_range(p, L, 4 * n + q, &lo[n], &hi[n]);
