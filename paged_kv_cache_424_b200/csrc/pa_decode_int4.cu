@@ -625,11 +625,13 @@ __global__ void __launch_bounds__(kWarps * 32, int4_ctas_per_sm(RT)) decode_int4
 // chunks of a block are one run of DRAM (measured, reads alone: 6.4 TB/s against
 // 5.9-6.2 with every warp on a context of its own; the 4-token 8B step 210 ->
 // 168 us).  The flat order: sequences, in each its head groups, in each
-// kStartCost places for what a context costs before its first block (its query
+// start_cost places for what a context costs before its first block (its query
 // rows, the first copies' latency) and then its blocks.  Team t owns places
 // [t W, (t + 1) W).
-constexpr int kStartCost = 8;
-constexpr int kMinShare = kStartCost + 8;
+// The start cost is 8 blocks' time, with 16 rows, whose queries and outputs are
+// four times as many, 14 (the 8B batch with 16 rows per KV head: 160 us at 5, 148
+// at 8, 141 at 14 and 18; with 4 rows: 81.4 at 5, 81.5 at 8, 82 at 12, 90 at 18).
+__host__ __device__ constexpr int int4_start_cost(int RT) { return RT == 4 ? 14 : 8; }
 
 // Blocks that sequence s's queries attend to, from which entry, and its length.
 struct Int4Seq {
@@ -640,7 +642,10 @@ __device__ __forceinline__ Int4Seq int4_seq(const DecodeParams &p, int s, bool r
     return {sp.L, sp.bfirst, min(sp.nblk - sp.bfirst, p.part_blocks)};
 }
 
-__device__ __forceinline__ int int4_share(int total, int teams) { return max(kMinShare, (total + teams - 1) / teams); }
+// A share is never less than a start and 8 blocks.
+__device__ __forceinline__ int int4_share(int total, int teams, int start_cost) {
+    return max(start_cost + 8, (total + teams - 1) / teams);
+}
 
 // places: int32 [num_seqs + 1] in the workspace, written for the merge: each
 // sequence's first place and the total.  (The host keeps totals that pass 30
@@ -649,7 +654,7 @@ template <typename T, int D, int RT, bool kMasked>
 __global__ void __launch_bounds__(kWarps * 32, int4_ctas_per_sm(RT))
     decode_int4_balanced_kernel(const DecodeParams p, int32_t *places, const int team_bits) {
     using E = Elem<T>;
-    constexpr int kThreads = kWarps * 32;
+    constexpr int kThreads = kWarps * 32, kCost = int4_start_cost(RT);
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int64_t chunk_end[kThreads];  // 64-bit: with half the static shared memory the compiler's code for the
     __shared__ int64_t warp_sum[kWarps];     // loop over blocks came out slower (7B batch 62 us against 69)
@@ -662,7 +667,7 @@ __global__ void __launch_bounds__(kWarps * 32, int4_ctas_per_sm(RT))
     const int per = (p.num_seqs + kThreads - 1) / kThreads, s0 = min(tid * per, p.num_seqs), s1 = min(s0 + per, p.num_seqs);
     const bool report = blockIdx.x == 0;
     int sum = 0;
-    for (int s = s0; s < s1; ++s) sum += groups * (kStartCost + int4_seq(p, s, report).n);
+    for (int s = s0; s < s1; ++s) sum += groups * (kCost + int4_seq(p, s, report).n);
     int scan = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -675,12 +680,12 @@ __global__ void __launch_bounds__(kWarps * 32, int4_ctas_per_sm(RT))
     chunk_end[tid] = scan;
     __syncthreads();
     const int total = (int)chunk_end[kThreads - 1];
-    const int teams = ((int)gridDim.x * kWarps) >> team_bits, share = int4_share(total, teams);
+    const int teams = ((int)gridDim.x * kWarps) >> team_bits, share = int4_share(total, teams, kCost);
     if (blockIdx.x == 0) {
         int at = scan - sum;
         for (int s = s0; s < s1; ++s) {
             places[s] = at;
-            at += groups * (kStartCost + int4_seq(p, s, false).n);
+            at += groups * (kCost + int4_seq(p, s, false).n);
         }
         if (tid == 0) places[p.num_seqs] = total;
         if (p.seq_order)  // results and shares do not depend on it; it is checked all the same
@@ -698,16 +703,16 @@ __global__ void __launch_bounds__(kWarps * 32, int4_ctas_per_sm(RT))
     int s = c * per;
     int at = c == 0 ? 0 : (int)chunk_end[c - 1];  // first place of sequence s
     Int4Seq seq = int4_seq(p, s, false);
-    while (x >= at + groups * (kStartCost + seq.n)) {
-        at += groups * (kStartCost + seq.n);
+    while (x >= at + groups * (kCost + seq.n)) {
+        at += groups * (kCost + seq.n);
         seq = int4_seq(p, ++s, false);
     }
-    int group = (x - at) / (kStartCost + seq.n);
-    at += group * (kStartCost + seq.n);  // first place of (s, group)
+    int group = (x - at) / (kCost + seq.n);
+    at += group * (kCost + seq.n);  // first place of (s, group)
     const int rows = p.group * p.q_len;
     T *out = reinterpret_cast<T *>(p.out);
     for (;;) {
-        const int blocks_at = at + kStartCost;
+        const int blocks_at = at + kCost;
         const int kvh = (group << team_bits) + member;
         const int from = max(0, x - blocks_at), to = min(seq.n, xend - blocks_at);
         if (seq.n == 0 && x <= at) {  // an empty context: zero rows
@@ -762,7 +767,8 @@ __global__ void __launch_bounds__(kWarps * 32, int4_ctas_per_sm(RT))
 // where the KV head's rows are no multiple of 4); where they have many, four
 // warps share one row's pieces.
 template <typename T, int D, int kRowWarps, int kRows>
-__global__ void __launch_bounds__(128) merge_int4_kernel(const DecodeParams p, const int32_t *places, const int teams, const int team_bits) {
+__global__ void __launch_bounds__(128) merge_int4_kernel(const DecodeParams p, const int32_t *places, const int teams, const int team_bits,
+                                                         const int start_cost) {
     using E = Elem<T>;
     constexpr int kV = D / 32;
     static_assert(kRowWarps == 1 || kRows == 1, "several warps share one row");
@@ -775,8 +781,8 @@ __global__ void __launch_bounds__(128) merge_int4_kernel(const DecodeParams p, c
     const int row = (blockIdx.x * (4 / kRowWarps) + warp / kRowWarps) * kRows;  // query row of the sequence, KV head by KV head
     const bool real = row < p.num_kv_heads * rows;
     const int kvh = real ? row / rows : 0, h = real ? row % rows : 0;
-    const int share = int4_share(places[p.num_seqs], teams);
-    const int at = places[s] + (kvh >> team_bits) * (kStartCost + seq.n) + kStartCost;
+    const int share = int4_share(places[p.num_seqs], teams, start_cost);
+    const int at = places[s] + (kvh >> team_bits) * (start_cost + seq.n) + start_cost;
     const int ta = at / share;
     const int pieces = seq.n == 0 || !real ? 0 : (at + seq.n - 1) / share - ta + 1;
     if (pieces <= 1) return;  // written by its warp; with four warps to a row it is all four that leave
@@ -879,9 +885,10 @@ cudaError_t launch_int4_t(const DecodeParams &p, int32_t *places, int ctas, cuda
     const int rows = p.num_heads * p.q_len, four = p.group * p.q_len % 4 == 0;
     const bool many = (int64_t)ctas * kWarps > 8 * (int64_t)p.num_seqs * p.num_kv_heads;
     const int32_t *at = places;
-    if (many) return launch_pdl(merge_int4_kernel<T, D, 4, 1>, dim3(rows, p.num_seqs), dim3(128), 0, stream, p, at, teams, team_bits);
-    if (four) return launch_pdl(merge_int4_kernel<T, D, 1, 4>, dim3((rows + 15) / 16, p.num_seqs), dim3(128), 0, stream, p, at, teams, team_bits);
-    return launch_pdl(merge_int4_kernel<T, D, 1, 1>, dim3((rows + 3) / 4, p.num_seqs), dim3(128), 0, stream, p, at, teams, team_bits);
+    const int cost = int4_start_cost(RT);
+    if (many) return launch_pdl(merge_int4_kernel<T, D, 4, 1>, dim3(rows, p.num_seqs), dim3(128), 0, stream, p, at, teams, team_bits, cost);
+    if (four) return launch_pdl(merge_int4_kernel<T, D, 1, 4>, dim3((rows + 15) / 16, p.num_seqs), dim3(128), 0, stream, p, at, teams, team_bits, cost);
+    return launch_pdl(merge_int4_kernel<T, D, 1, 1>, dim3((rows + 3) / 4, p.num_seqs), dim3(128), 0, stream, p, at, teams, team_bits, cost);
 }
 
 template <typename T, int D>
