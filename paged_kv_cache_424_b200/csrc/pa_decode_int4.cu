@@ -34,7 +34,12 @@
 // with 5th-generation MMAs the codes would be written back to shared memory,
 // widened, before the MMA could read them, and each 128-token chunk would
 // wait for S to come back from TMEM and for P to go in; the FP8 kernel that is
-// built so takes 97 us for the 8B step, over about twice the bytes.
+// built so takes 97 us for the 8B step, over about twice the bytes; this one 82
+// (4.8 TB/s of 4-bit rows; 7B batch 63 us, 70B long context 64, four draft
+// tokens 140).  What bounds it: with up to 8 rows the unpacking and the copies'
+// issue beside DRAM (steady state 0.81 of the copy rate), with 16 the matrix
+// instructions and two CTAs' worth of warps per SM (0.56); then what each
+// context's start costs.
 //
 // Weights are f16 under a power of two that follows the largest V scale seen.
 // A code is 0..15 and not -8..7, so a weight's rounding error would count 7.5
