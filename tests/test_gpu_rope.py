@@ -382,3 +382,18 @@ def test_graph_and_other_stream():
     call(stream=side)
     side.synchronize()
     assert torch.equal(qo, want_q) and torch.equal(kc, want_k)
+
+
+@pytest.mark.parametrize("inter,R", [(False, 128), (True, 128), (False, 20)])
+def test_keys_alone_and_both_in_place(inter, R):
+    """Keys without queries (one head, many heads, many tokens), and queries and keys both in place."""
+    g = gen(78)
+    f = freqs(R)
+    for T, H, Hk in ((1, 1, 1), (3000, 8, 1), (17, 32, 32)):
+        q, k = rand(g, (T, H, 128), torch.bfloat16), rand(g, (T, Hk, 128), torch.bfloat16)
+        pos = torch.randint(0, 9000, (T,), generator=g, device="cuda")
+        _, alone = check_rope(None, k, pos, f, inter, what="keys alone")
+        qo, ko = check_rope(q, k, pos, f, inter, what="both")
+        assert torch.equal(ko, alone)
+        pa().pa_rope(q, q, k, k, pos, f, interleaved=inter)
+        assert torch.equal(q, qo) and torch.equal(k, ko)
