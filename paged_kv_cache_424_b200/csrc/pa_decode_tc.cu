@@ -328,10 +328,10 @@ __global__ void __launch_bounds__(tc_threads(G, kFp8), tc_ctas_per_sm(G, kFp8))
     const int H = p.num_heads, head0 = kvh * G;  // head0: unmasked launches (group == G, q_len == 1)
     T *out = reinterpret_cast<T *>(p.out);
     pdl_launch_dependents();
-    // Until pdl_wait() below the CTA reads only inputs that no kernel of this
-    // library writes (seq_order, block table, context length, q), so this
-    // part overlaps the tail of the kernel before it on the stream; the
-    // caches, the output and the workspace are touched after the wait.
+    // Every input may come from the kernel in front of this one (q from a
+    // rotation, lengths and tables from the caller's own kernels), and only what
+    // stands behind the wait sees its writes.
+    pdl_wait();
     const int s = scheduled_seq(p, g_seq, part0 == 0 && g_head == 0 && tid == 0);
     if (s < 0) return;
     // Without a window a CTA's slice of the table starts at part0 *
@@ -384,7 +384,6 @@ __global__ void __launch_bounds__(tc_threads(G, kFp8), tc_ctas_per_sm(G, kFp8))
             }
         }
     }
-    pdl_wait();
     if (L == 0) {
         for (int i = tid; i < rows * kD; i += blockDim.x) out[row_of(i / kD) * kD + i % kD] = E::from_float(0.f);
         return;

@@ -270,10 +270,7 @@ __global__ void __launch_bounds__(kThreads, 8) rope_kernel(const RopeParams p) {
     constexpr int kRows = kThreads / LPR;  // rows of a pass
     __shared__ __align__(16) float cos_s[2][kMaxHalf], sin_s[2][kMaxHalf];
     const int tid = threadIdx.x, lane = tid & 31;
-    // The decode kernels read q before they wait for the kernel in front of
-    // them, so a kernel that writes q or k does not let the next one start
-    // early; a cache write alone does.
-    if (!p.q_out && !p.k_out) pdl_launch_dependents();
+    pdl_launch_dependents();
     const int half = p.half;
     // this lane's pieces ca and cb of 8 dims: half: piece j and the one half / 8
     // behind it, which hold both ends of pairs 8 j .. 8 j + 7 (j < half / 8; the
