@@ -288,10 +288,14 @@ pa_status pa_decode_ext(void *out, const void *q, const void *k_cache, const voi
  * row: every element to within 2^-14 of the row's largest |q| (exact for fp16
  * elements within 2^4 of it, for bf16 ones within 2^7), and the products with
  * the codes are exact.  The softmax weight times the V scale is rounded to
- * fp16, with up to 4 query rows per KV head to two fp16 parts (22 bits); what
- * the rounding of more rows takes is given back at the middle code, so its
- * error is at most 2^-11 of the weight times 7.5 codes.  Logits, sums and the
- * output are fp32.  A row that attends to a row of NaN is NaN.
+ * fp16 under a factor of its own query row, chosen by the largest such product
+ * T among the tokens that the row attends to (a scale counts at least as 2^-20
+ * of the row's |low|, and as 2^-70).  With up to 4 query rows per KV head it
+ * takes two fp16 parts, off by at most 2^-22 of itself or 2^-42 T.  With more it
+ * takes one, off by at most 2^-11 of itself or 2^-31 T, and what the rounding
+ * takes is given back at the middle code, so that 7.5 codes of it are left at
+ * the most.  Logits, sums and the output are fp32.  A row that attends to a row
+ * of NaN is NaN.
  * partition_tokens: 0 = automatic: equal shares of all blocks of the batch,
  * whatever the lengths (one context is not cut at fixed positions).
  * Workspace as from pa_decode_workspace_size with the same dims.

@@ -4,6 +4,7 @@
 // With codes u, row scales s, s' and lowest values l, l' (K and V),
 //   x_t = c (s_t (q . u_t) + l_t sum(q)),   c = scale log2(e) k_scale
 //   out = sum_t p_t (s'_t u'_t + l'_t) / sum_t p_t,   p_t = 2^(x_t - m)
+// for any m; see below for the one taken.
 // so the codes enter both products as integers 0..15 and the scales act on
 // tokens: on a logit after the first product, on a weight before the second.
 //
@@ -11,7 +12,7 @@
 // instructions; for each block
 //   S^T (16 tokens x rows) = U (16 x D) . Q^T       m16n8k32, u8 x s8 -> s32
 //   O^T (D x rows)        += U'^T (D x 16) . W^T    m16n8k16, f16 -> f32
-// with W = p s'.  Unpacking is what bounds such a kernel (logic runs at half
+// with W = 2^-24 p s'.  Unpacking is what bounds such a kernel (logic runs at half
 // the issue rate), so the nibbles are used where they stand:
 //   - K: w & 0x0f0f0f0f are four codes as bytes, w & 0xf0f0f0f0 four codes
 //     times 16 as unsigned bytes: one instruction for four.  The two halves
@@ -41,12 +42,20 @@
 // instructions and two CTAs' worth of warps per SM (0.56); then what each
 // context's start costs.
 //
-// Weights are f16 under a power of two that follows the largest V scale seen.
+// Weights are f16, and so that they stay inside its range a row's m follows the
+// running maximum of x_t + log2 |s'_t| of the tokens that the row attends to, not
+// that of x_t: a V scale counts as far as the row's softmax lets it, and one that
+// the row does not see not at all.  The largest weight stands between 2^6 and
+// 2^15; below 2^-14 f16 loses bits and below 2^-25 everything, which is then
+// under 2^-31 of that largest.  (s' counts at least as 2^-20 |l'|, so that the
+// sum of p l' keeps inside fp32, and as 2^-70: fp32 holds p from 2^-126 to 2^127,
+// the factor 2^-24 shares that range out between large and small scales.)
 // A code is 0..15 and not -8..7, so a weight's rounding error would count 7.5
 // codes where a centred code's would cancel.  With up to 4 rows the rounding's
-// remainder takes the second column of each row (hi + lo: 22 bits); with more,
-// the weights' sum before and after the rounding (the latter by one more MMA
-// against ones) says what it took, which is given back at the middle code 7.5.
+// remainder, times 2^11, takes the second column of each row (hi + 2^-11 lo: 22
+// bits, down to 2^-42 of the largest); with more, the weights' sum before and
+// after the rounding (the latter by one more MMA against ones) says what it took,
+// which is given back at the middle code 7.5.
 //
 // Two kernels share the warp's work.  decode_int4_kernel: CTA = (partition, KV
 // head, sequence), the warps take every 4th pair of blocks and merge their
@@ -70,7 +79,12 @@ namespace {
 constexpr int kWarps = kInt4Warps;
 constexpr int kStages = 3;  // per warp, of two blocks each: up to 12 chunks in flight
 constexpr float kTwo24 = 16777216.f;
-constexpr float kMaxWeightScale = 64.f;  // times p <= 2^8 stays inside f16
+constexpr float kScaleUnit = 1.f / kTwo24;  // of s' in W
+constexpr float kLowUnit = 0x1p-44f;        // what |l'| counts as in W's range
+constexpr float kLeastScale = 0x1p-94f;     // what any token counts as
+constexpr float kNewWeight = 6.f;           // a new m puts the largest weight at 2^6,
+constexpr float kMaxWeight = 15.f;          // and 2^15 calls for a new one: inside f16, as the remainder times 2^11 is
+constexpr float kLowPart = 2048.f;
 
 // D += A B, one m16n8k16 of f16.
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -178,8 +192,6 @@ struct Int4Warp {
     int lo[RT], hi[RT];   // attended positions
     int lo_any, lo_all, hi_all;  // seen by some row from lo_any; by all rows in [lo_all, hi_all]
     float m[RT], l[RT], z[RT], zw[RT], acc[NP][MT][4], accw[NP][4];
-    float cv;     // power of two the V scales are multiplied by (warp-uniform)
-    float limit;  // V scale above which it is chosen anew
 
     // Query rows of (s, kvh): q = (128 hi + lo) 2^-e; this lane makes part r & 1 of
     // row 4 n + r / 2, the dims it holds of K, per word (8 dims) the even dims'
@@ -248,8 +260,6 @@ struct Int4Warp {
             lo_all = p.window > 0 ? L - p.window : 0;
             hi_all = L - p.q_len;
         }
-        cv = 1.f;
-        limit = 0.f;
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
 #pragma unroll
@@ -329,7 +339,7 @@ struct Int4Warp {
                 for (int n = 0; n < RT; ++n) dead[n][i] = tok >= tend || (kMasked && (tok < lo[n] || tok > hi[n]));
             }
         }
-        auto logits = [&](int n) {  // +inf before the first maximum
+        auto logits = [&](int n) {  // +inf before the first m
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[n][i] = fmaf(ke[i].x * fac[n], raw[n][i], fmaf(ke[i].y, off_q[n], -m[n]));
             if constexpr (kEdge) {
@@ -338,8 +348,8 @@ struct Int4Warp {
                     if (dead[n][i]) x[n][i] = -INFINITY;
             }
         };
-        // running maxima, raised only when a logit beats one by 2^8 or a V
-        // scale its power of two (NaN takes this way too)
+        // m is raised only when a weight leaves its range: looked at is the lane's
+        // largest p times its largest scale, by exponents (NaN takes this way too)
         float most = -INFINITY;
 #pragma unroll
         for (int n = 0; n < RT; ++n) {
@@ -347,39 +357,33 @@ struct Int4Warp {
             most = max3_nan(most, x[n][0], x[n][1]);
             most = max3_nan(most, x[n][2], x[n][3]);
         }
-        const float big4 = fmaxf(fmaxf(fabsf(ce[0].x), fabsf(ce[1].x)), fmaxf(fabsf(ce[2].x), fabsf(ce[3].x)));
-        if (__any_sync(0xffffffffu, big4 > limit || !(most <= kLazyMax))) {
-            float big = big4;
+        const float big_s = max3_nan(max3_nan(fabsf(ce[0].x), fabsf(ce[1].x), fabsf(ce[2].x)), fabsf(ce[3].x), kLeastScale / kScaleUnit);
+        const float big_l = max3_nan(max3_nan(fabsf(ce[0].y), fabsf(ce[1].y), fabsf(ce[2].y)), fabsf(ce[3].y), 0.f);
+        const float big4 = max3_nan(big_s, big_l * (kLowUnit / kScaleUnit), 0.f);  // in [2^(e - 127), 2^(e - 126)), e its exponent bits
+        const float e4 = __uint_as_float(0x4b000000u + (__float_as_uint(big4) >> 23));  // 2^23 + e
+        if (__any_sync(0xffffffffu, !(most <= (8388608.f + kMaxWeight + 24.f + 126.f) - e4))) {
+            float lg[4];  // what a token's scale adds to its logit
 #pragma unroll
-            for (int o = 16; o > 2; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-            float turn = 1.f;  // new power of two over the old one
-            if (big > limit) {
-                const float was = cv;
-                int e;
-                (void)frexpf(fminf(big, FLT_MAX), &e);
-                cv = ldexpf(1.f, -min(max(e, -120), 126));  // |scale| cv in [0.5, 1), or up to 4 at the range's end
-                limit = kMaxWeightScale / cv;
-                turn = cv / was;
-            }
+            for (int i = 0; i < 4; ++i)
+                lg[i] = __log2f(max3_nan(fabsf(ce[i].x) * kScaleUnit, fabsf(ce[i].y) * kLowUnit, kLeastScale));
 #pragma unroll
             for (int n = 0; n < RT; ++n) {
-                float bm = -INFINITY;
+                float top = -INFINITY;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float v = fmaf(ke[i].x * fac[n], raw[n][i], ke[i].y * off_q[n]);
+                    float v = fmaf(ke[i].x * fac[n], raw[n][i], ke[i].y * off_q[n]) + lg[i];
                     if (kEdge && dead[n][i]) v = -INFINITY;
-                    bm = fmaxf(bm, v != v ? 0.f : v);  // a NaN row gets a finite maximum and NaN sums
+                    top = fmaxf(top, v != v ? 0.f : v);  // a NaN row gets a finite m and NaN sums
                 }
 #pragma unroll
-                for (int o = 16; o > 2; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, o));
+                for (int o = 16; o > 2; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                 float alpha = 1.f;
-                if (bm > m[n] + kLazyMax) {  // a row's maximum does not depend on the other rows
-                    alpha = ex2(m[n] - bm);  // 0 on the first block
-                    m[n] = bm;
+                if (top > m[n] + kMaxWeight) {  // a row's m does not depend on the other rows
+                    alpha = ex2(m[n] - (top - kNewWeight));  // 0 on the first block
+                    m[n] = top - kNewWeight;
                 }
                 l[n] *= alpha;
                 z[n] *= alpha;
-                alpha *= turn;
                 zw[n] *= alpha;
                 if constexpr (kSplit) {
 #pragma unroll
@@ -422,7 +426,7 @@ struct Int4Warp {
         uint32_t wb[NP][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float sv = ce[i].x * cv;
+            const float sv = ce[i].x * kScaleUnit;
             float w[RT];
 #pragma unroll
             for (int n = 0; n < RT; ++n) {
@@ -436,7 +440,7 @@ struct Int4Warp {
             }
 #pragma unroll
             for (int n = 0; n < NP; ++n) {
-                const __half2 h = kSplit ? __floats2half2_rn(w[0], w[0] - __half2float(__float2half_rn(w[0])))
+                const __half2 h = kSplit ? __floats2half2_rn(w[0], (w[0] - __half2float(__float2half_rn(w[0]))) * kLowPart)
                                          : __floats2half2_rn(w[(2 * n) % RT], w[(2 * n + 1) % RT]);
                 wb[n][i] = transpose8x8(*reinterpret_cast<const uint32_t *>(&h));
             }
@@ -532,17 +536,17 @@ struct Int4Warp {
                 z[n] += __shfl_xor_sync(0xffffffffu, z[n], o);
                 if constexpr (!kSplit) zw[n] += __shfl_xor_sync(0xffffffffu, zw[n], o);
             }
-            if constexpr (!kSplit) z[n] = fmaf(7.5f * (zw[n] - accw[n / 2][n & 1]), 1.f / cv, z[n]);
+            if constexpr (!kSplit) z[n] = fmaf(zw[n] - accw[n / 2][n & 1], 7.5f / kScaleUnit, z[n]);
         }
     }
     __device__ __forceinline__ float4 output(int n, int g) const {
-        const float back = 1.f / cv;  // a power of two
+        constexpr float kUnit = kTwo24 / kScaleUnit;
         float o[4];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const float *c = acc[n / 2][2 * g + u];
-            o[2 * u] = fmaf((kSplit ? c[0] + c[1] : c[n & 1]) * kTwo24, back, z[n]);
-            o[2 * u + 1] = fmaf((kSplit ? c[2] + c[3] : c[2 + (n & 1)]) * (kTwo24 / 16.f), back, z[n]);
+            const float *a = acc[n / 2][2 * g + u];
+            o[2 * u] = fmaf(kSplit ? fmaf(a[1], 1.f / kLowPart, a[0]) : a[n & 1], kUnit, z[n]);
+            o[2 * u + 1] = fmaf(kSplit ? fmaf(a[3], 1.f / kLowPart, a[2]) : a[2 + (n & 1)], kUnit / 16.f, z[n]);
         }
         return make_float4(o[0], o[1], o[2], o[3]);
     }
@@ -598,12 +602,18 @@ __global__ void __launch_bounds__(kWarps * 32, int4_ctas_per_sm(RT)) decode_int4
     for (int n = 0; n < RT; ++n) {
         const int h = 4 * n + q;
         if (h >= rows) continue;
+        // each warp's quotient and log-sum-exp: the m of two warps may be further apart than fp32's exponents
+        const float inv = w.l[n] == 0.f ? 0.f : 1.f / w.l[n];
 #pragma unroll
-        for (int g = 0; g < D / 32; ++g)
-            *reinterpret_cast<float4 *>(red_acc + (warp * RW + h) * D + 32 * g + 4 * r) = w.output(n, g);
+        for (int g = 0; g < D / 32; ++g) {
+            const float4 v = w.output(n, g);
+            *reinterpret_cast<float4 *>(red_acc + (warp * RW + h) * D + 32 * g + 4 * r) =
+                w.l[n] == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+        }
         if (r == 0) {
-            red_m[warp * RW + h] = w.m[n];
-            red_l[warp * RW + h] = w.l[n];
+            const float lse = w.l[n] == 0.f ? -INFINITY : w.m[n] + log2f(w.l[n]);
+            red_m[warp * RW + h] = lse != lse ? 0.f : lse;  // the NaN is in the quotient
+            red_l[warp * RW + h] = w.l[n] == 0.f ? 0.f : 1.f;
         }
     }
     __syncthreads();
