@@ -285,9 +285,9 @@ pa_status pa_decode_ext(void *out, const void *q, const void *k_cache, const voi
  * about a quarter of the bytes of a 16-bit cache.  Every group size and
  * head_dim runs on kernels that feed the codes to the matrix units as exact
  * integers.  The query is rounded to integers under a power-of-two factor per
- * row: every element to within 2^-14 of the row's largest |q| (exact for fp16
- * elements within 2^4 of it, for bf16 ones within 2^7), and the products with
- * the codes are exact.  The softmax weight times the V scale is rounded to
+ * row: every element to within 1 / 32640 of the row's largest |q| (exact for
+ * fp16 elements down to a 15th of it, for bf16 ones down to a 127th), and the
+ * products with the codes are exact.  The softmax weight times the V scale is rounded to
  * fp16 under a factor of its own query row, chosen by the largest such product
  * T among the tokens that the row attends to (a scale counts at least as 2^-20
  * of the row's |low|, and as 2^-70).  With up to 4 query rows per KV head it

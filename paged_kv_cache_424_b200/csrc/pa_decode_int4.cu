@@ -16,11 +16,12 @@
 // the issue rate), so the nibbles are used where they stand:
 //   - K: w & 0x0f0f0f0f are four codes as bytes, w & 0xf0f0f0f0 four codes
 //     times 16 as unsigned bytes: one instruction for four.  The two halves
-//     add up in accumulators of their own.  Q goes in as two s8 parts, q =
-//     (128 hi + lo) 2^-e rounded to 15 bits of the row's largest |q| (exact for
-//     fp16 elements within 2^4 of it, for bf16 ones within 2^7); a row's two
-//     parts are two columns of the product, so 8 columns hold 4 rows and a
-//     lane gets both parts of one row and adds them as integers.
+//     add up in accumulators of their own.  Q goes in as two s8 parts, q = (256
+//     hi + lo) 2^-e rounded to integers of at most 32639, the largest |q| of a row
+//     at 16320 or above (exact for fp16 elements down to a 15th of it, for bf16
+//     ones down to a 127th); a row's two parts are two columns of the product, so
+//     8 columns hold 4 rows and a lane gets both parts of one row and adds them as
+//     integers.
 //   - V pairs two tokens in a register: a transposing matrix load of 16-bit
 //     elements brings four codes of one token and the same four dims' codes of
 //     the next into one word, and w & 0x000f000f or w & 0x00f000f0 is then a
@@ -193,7 +194,7 @@ struct Int4Warp {
     int lo_any, lo_all, hi_all;  // seen by some row from lo_any; by all rows in [lo_all, hi_all]
     float m[RT], l[RT], z[RT], zw[RT], acc[NP][MT][4], accw[NP][4];
 
-    // Query rows of (s, kvh): q = (128 hi + lo) 2^-e; this lane makes part r & 1 of
+    // Query rows of (s, kvh): q = (256 hi + lo) 2^-e; this lane makes part r & 1 of
     // row 4 n + r / 2, the dims it holds of K, per word (8 dims) the even dims'
     // bytes and the odd dims'.  logit = s T fac + low off with T = 16 q . u (u
     // alone with kOneSum: q . u) as an integer.
@@ -220,17 +221,17 @@ struct Int4Warp {
             const bool fine = mx <= FLT_MAX;  // no NaN, no infinity
             int e = 0;
             if (mx > 0.f && fine) {
-                (void)frexpf(mx, &e);  // mx in [2^(e-1), 2^e)
-                e = min(14 - e, 120);  // mx 2^e in [2^13, 2^14)
+                const float half = frexpf(mx, &e);  // mx = half 2^e, half in [1/2, 1)
+                e = min((half > 32639.f / 32768.f ? 14 : 15) - e, 120);
             }
-            // 1.5 2^23 + v holds the integer v in its low bits.  The largest |q| is
-            // a 16-bit number, so its v is exact and at most 16376, and with it
-            // every |v|: the high part fits s8.  (A row that is not fine may give
-            // anything: its factor is NaN.)
+            // 1.5 2^23 + v holds the integer v in its low bits.  |v| <= 32639, so
+            // that v = 256 hi + lo with both parts in s8: lo the low byte, hi the
+            // next one of v + 128.  (A row that is not fine may give anything: its
+            // factor is NaN.)
             constexpr float kInt = 12582912.f;
             const float up = ldexpf(1.f, e);
-            const uint32_t part_mask = (r & 1) ? 0x7f7f7f7fu : 0xffffffffu;
-            const int part_shift = (r & 1) ? 0 : 7;
+            const uint32_t part_add = (r & 1) ? 0 : 128;
+            const int part_shift = (r & 1) ? 0 : 8;
             uint32_t sum = 0;
 #pragma unroll
             for (int w = 0; w < KW; ++w)
@@ -241,9 +242,9 @@ struct Int4Warp {
                     for (int i = 0; i < 4; ++i) {
                         const uint32_t k = __float_as_uint(fmaf(y[8 * w + 2 * i + odd], up, kInt));
                         sum += k;
-                        v[i] = k >> part_shift;
+                        v[i] = (k + part_add) >> part_shift;
                     }
-                    qb[n][2 * w + odd] = __byte_perm(__byte_perm(v[0], v[1], 0x0040), __byte_perm(v[2], v[3], 0x0040), 0x5410) & part_mask;
+                    qb[n][2 * w + odd] = __byte_perm(__byte_perm(v[0], v[1], 0x0040), __byte_perm(v[2], v[3], 0x0040), 0x5410);
                 }
             sum -= (uint32_t)(D / 4) * 0x4b400000u;  // the constant's bits
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
@@ -324,8 +325,8 @@ struct Int4Warp {
             for (int n = 0; n < RT; ++n)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int e = ev[n][2 * i] * 128 + ev[n][2 * i + 1];
-                    raw[n][2 * b + i] = (float)(kOneSum ? e : e * 16 + (od[n][2 * i] * 128 + od[n][2 * i + 1]));
+                    const int e = ev[n][2 * i] * 256 + ev[n][2 * i + 1];
+                    raw[n][2 * b + i] = (float)(kOneSum ? e : e * 16 + (od[n][2 * i] * 256 + od[n][2 * i + 1]));
                 }
         }
         bool dead[RT][4];
