@@ -247,7 +247,11 @@ typedef struct pa_decode_opts {
                                  sequences are scheduled (see pa_prefix_order); results do not
                                  depend on it.  Entries outside [0, num_seqs) are skipped and
                                  flagged (PA_DEVERR_CONTEXT); a sequence it does not list gets
-                                 no defined output */
+                                 no defined output.  Over a 4-bit cache with partition_tokens = 0
+                                 the entries are checked and flagged, but where the batch is cut
+                                 into equal shares (contexts that may pass 128 tokens) the shares
+                                 follow the batch's own order; give a partition size to have the
+                                 sequences scheduled in seq_order */
 } pa_decode_opts;
 
 /* Workspace bytes pa_decode_ext needs (0 = none), (size_t)-1 for invalid
@@ -297,7 +301,8 @@ pa_status pa_decode_ext(void *out, const void *q, const void *k_cache, const voi
  * the most.  Logits, sums and the output are fp32.  A row that attends to a row
  * of NaN is NaN.
  * partition_tokens: 0 = automatic: equal shares of all blocks of the batch,
- * whatever the lengths (one context is not cut at fixed positions).
+ * whatever the lengths (one context is not cut at fixed positions), laid out
+ * in the batch's order.
  * Workspace as from pa_decode_workspace_size with the same dims.
  */
 pa_status pa_decode_int4(void *out, const void *q, const void *k_cache, const void *v_cache,
@@ -313,7 +318,9 @@ pa_status pa_decode_int4(void *out, const void *q, const void *k_cache, const vo
  *     scale = bf16((max x - low) / 15)
  *     code  = clamp(round_half_even((x - low) / scale), 0, 15)   (0 where scale == 0)
  * and the same for value.  A row with a NaN or an infinity gets scale and low
- * NaN (code 0): it reads back as NaN.  One kernel on `stream`.
+ * NaN (code 0): it reads back as NaN.  Negative slots are skipped (padding
+ * tokens), slots past the pool are skipped and flagged (PA_DEVERR_SLOT).  Slots
+ * must be distinct: two tokens writing one slot race.  One kernel on `stream`.
  */
 pa_status pa_reshape_and_cache_int4(const void *key, const void *value, void *k_cache, void *v_cache,
                                     const int64_t *slot_mapping, int32_t num_tokens, const pa_dims *dims,
