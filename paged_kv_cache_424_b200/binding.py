@@ -344,6 +344,14 @@ def pa_decode_fp8(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_c
     return out
 
 
+def _int4_arguments(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    block_tables: torch.Tensor, context_lens: torch.Tensor) -> None:
+    """What has to go together in an attention call over a 4-bit cache."""
+    if out.shape != q.shape or out.dtype != q.dtype or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or \
+            block_tables.dim() != 2 or block_tables.shape[0] != q.shape[0] or context_lens.numel() != q.shape[0]:
+        raise ValueError("out must be as q, v_cache as k_cache, block_tables [num_seqs, blocks], context_lens [num_seqs]")
+
+
 def pa_decode_int4(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                    block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float, num_kv_heads: int,
                    max_context_len: int, partition_tokens: int = 0, workspace: Optional[torch.Tensor] = None,
@@ -358,9 +366,7 @@ def pa_decode_int4(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_
     NB, Hk, nbytes = k_cache.shape
     if nbytes != 8 * D + 64:
         raise ValueError("q and k_cache disagree on head_dim")
-    if out.shape != q.shape or out.dtype != q.dtype or v_cache.shape != k_cache.shape or block_tables.dim() != 2 or \
-            block_tables.shape[0] != S or context_lens.numel() != S:
-        raise ValueError("out must be as q, v_cache as k_cache, block_tables [num_seqs, blocks], context_lens [num_seqs]")
+    _int4_arguments(out, q, k_cache, v_cache, block_tables, context_lens)
     _on_device(q, out, k_cache, v_cache, block_tables, context_lens, workspace)
     _dense(out, q, k_cache, v_cache, block_tables, context_lens, workspace)
     dims = _dims_ref(S, H, Hk, D, 16, block_tables.shape[1], NB, _dtype_code(q), PA_INT4)
@@ -402,6 +408,8 @@ def pa_decode_ext(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_c
         raise TypeError("block_tables and context_lens must be int32")
     if q.dim() != 4 or q.shape[1] != q_len or tuple(out.shape) != tuple(q.shape):
         raise ValueError("q and out must be [num_seqs, q_len, num_heads, head_dim]")
+    if _is_int4(k_cache):
+        _int4_arguments(out, q, k_cache, v_cache, block_tables, context_lens)
     dims = ext_dims(q, k_cache, block_tables)
     if seq_order is not None:
         _need_cuda(seq_order)
