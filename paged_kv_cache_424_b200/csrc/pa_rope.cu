@@ -548,11 +548,14 @@ template <typename T, int D, int kCache>
 cudaError_t launch_rope_c(const RopeParams &p, cudaStream_t stream) {
     constexpr int kRows = kThreads / (D / 16);
     const int total = p.num_heads + (kCache == kCacheNone ? 1 : 2) * p.num_kv_heads;
-    // few tokens: a CTA per pass over a token's rows, to reach more SMs (each
-    // computes the sines again); many: a resident wave that walks over them
+    // many tokens: a resident wave that walks over them; fewer: as many CTAs to a
+    // token's passes as still make one wave, each of which computes the sines again
+    // (32 + 32 + 32 heads of 128 into FP8, a token's 6 passes in one CTA against the
+    // rule's: 171 tokens 7.1 us and 4.3, 256 10.0 and 5.5, 512 11.1 and 7.3; 342
+    // tokens of 32 + 8 heads 4.3 and 3.2)
     const int passes = (total + kRows - 1) / kRows;
-    const bool few = (int64_t)p.num_tokens * passes <= 1024;
-    const dim3 grid(few || p.num_tokens < kWave ? p.num_tokens : kWave, few ? passes : 1), block(kThreads);
+    const int per_token = std::max(1, std::min(passes, kWave / p.num_tokens));
+    const dim3 grid(std::min(p.num_tokens, kWave), per_token), block(kThreads);
     const int pairs = p.interleaved ? kPairsInterleaved : p.half % 8 == 0 ? kPairsHalf : kPairsHalfOdd;
     switch (pairs) {
         case kPairsHalf: return launch_pdl(rope_kernel<T, D, kCache, kPairsHalf>, grid, block, 0, stream, p);
