@@ -36,9 +36,9 @@
 // with 5th-generation MMAs the codes would be written back to shared memory,
 // widened, before the MMA could read them, and each 128-token chunk would
 // wait for S to come back from TMEM and for P to go in; the FP8 kernel that is
-// built so takes 97 us for the 8B step, over about twice the bytes; this one 82
-// (4.8 TB/s of 4-bit rows; 7B batch 63 us, 70B long context 64, four draft
-// tokens 140).  What bounds it: with up to 8 rows the unpacking and the copies'
+// built so takes 97 us for the 8B step, over about twice the bytes; this one 80
+// (4.9 TB/s of 4-bit rows; 7B batch 62 us, 70B long context 64, four draft
+// tokens 143).  What bounds it: with up to 8 rows the unpacking and the copies'
 // issue beside DRAM (steady state 0.81 of the copy rate), with 16 the matrix
 // instructions and two CTAs' worth of warps per SM (0.56); then what each
 // context's start costs.
@@ -645,8 +645,8 @@ __global__ void __launch_bounds__(kWarps * 32, int4_ctas_per_sm(RT)) decode_int4
 // rows, the first copies' latency) and then its blocks.  Team t owns places
 // [t W, (t + 1) W).
 // The start cost is 8 blocks' time, with 16 rows, whose queries and outputs are
-// four times as many, 14 (the 8B batch with 16 rows per KV head: 160 us at 5, 148
-// at 8, 141 at 14 and 18; with 4 rows: 81.4 at 5, 81.5 at 8, 82 at 12, 90 at 18).
+// four times as many, 14 (the 8B batch with 16 rows per KV head: 160 us at 5, 150
+// at 8, 143 at 14, 145 at 18; with 4 rows: 79 at 5, 80 at 8, 81 at 12, 92 at 18).
 __host__ __device__ constexpr int int4_start_cost(int RT) { return RT == 4 ? 14 : 8; }
 
 // Blocks that sequence s's queries attend to, from which entry, and its length.
@@ -673,7 +673,7 @@ __global__ void __launch_bounds__(kWarps * 32, int4_ctas_per_sm(RT))
     constexpr int kThreads = kWarps * 32, kCost = int4_start_cost(RT);
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int64_t chunk_end[kThreads];  // 64-bit: with half the static shared memory the compiler's code for the
-    __shared__ int64_t warp_sum[kWarps];     // loop over blocks came out slower (7B batch 62 us against 69)
+    __shared__ int64_t warp_sum[kWarps];     // loop over blocks came out slower (7B batch 62 us against 69.5, 8B 80.5 against 90.5)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, q = lane & 3;
     pdl_launch_dependents();
     const uint32_t ring = smem_addr(smem) + warp * kStages * 4 * int4_chunk_bytes(D);

@@ -555,8 +555,8 @@ cudaError_t launch_rope_c(const RopeParams &p, cudaStream_t stream) {
     // many tokens: a resident wave that walks over them; fewer: as many CTAs to a
     // token's passes as still make one wave, each of which computes the sines again
     // (32 + 32 + 32 heads of 128 into FP8, a token's 6 passes in one CTA against the
-    // rule's: 171 tokens 7.1 us and 4.3, 256 10.0 and 5.5, 512 11.1 and 7.3; 342
-    // tokens of 32 + 8 heads 4.3 and 3.2)
+    // rule's: 171 tokens 7.1 us and 4.3, 256 7.4 and 5.0, 512 8.4 and 7.0; 342
+    // tokens of 32 + 8 heads 4.2 and 3.2)
     const int passes = (total + kRows - 1) / kRows;
     const int per_token = std::max(1, std::min(passes, kWave / p.num_tokens));
     const dim3 grid(std::min(p.num_tokens, kWave), per_token), block(kThreads);
