@@ -183,3 +183,28 @@ def test_second_part_of_a_weight(group, D):
     out = (torch.einsum("hgt,thd->hgd", w, codes) + torch.einsum("hgt,th->hg", pr, ends[..., 1])[..., None]) / pr.sum(-1, keepdim=True)
     far = (out.reshape(1, 2 * group, D) - want).abs() - slack - 2.0 ** -11 * (want.abs() + slack) - 2.0 ** -25
     assert bool((far > 0).any())
+
+
+@pytest.mark.parametrize("group,q_len", ROWS)
+@pytest.mark.parametrize("P", [0, 4096])
+def test_rows_of_zeros(group, q_len, P):
+    """V rows of nothing but zeros under rising logits give zeros; a last row that is not zero gives its share, whether
+    it holds the softmax or a 2^-20 of it."""
+    D, n = 64, 30000
+    g = gen(P)
+    kc, vc = kw.pools(g, n, 1, D)
+    N = kc.shape[0] * 16
+    low = torch.linspace(-30.0, 30.0, N)
+    zeros = torch.zeros(N)
+    kw.set_rows(kc, zeros, low)
+    kw.set_rows(vc, zeros, zeros)
+    q = queries(q_len, group, D, torch.bfloat16)
+    table = torch.arange(kc.shape[0], dtype=torch.int32, device="cuda")[None]
+    out = run(q[None], kc, vc, table, torch.tensor([n], dtype=torch.int32, device="cuda"), 1.0, q_len, 0, P)
+    assert not out.any()
+    for at, logit in ((n - q_len, 45.0), (n - q_len, 16.0), (0, 45.0), (0, 16.0)):
+        k2, s = low.clone(), zeros.clone()
+        k2[at], s[at] = logit, 1.0
+        kw.set_rows(kc, zeros, k2)
+        kw.set_rows(vc, s, -7.5 * s)
+        check(q, kc, vc, n, 1.0, f"one row at {at}, logit {logit}", q_len=q_len, P=P)
